@@ -17,7 +17,10 @@
  * gptq_export_checkpoint (the outputs in the loaders' checkpoint layout),
  * gptq_quantize_layer_noalloc (quantize on a fixed library scratch),
  * gptq_workspace_bytes / gptq_validate_config (host-side sizing and checks)
- * and gptq_selftest_wait_timeout (the bounded-wait failure path).
+ * and gptq_selftest_wait_timeout (the bounded-wait failure path).  A solved
+ * layer runs on 8-bit integer tensor cores through the calls at the end:
+ * gptq_layout_int8, gptq_quantize_tokens, gptq_norm_tokens,
+ * gptq_matmul_int8 and gptq_matmul_int8_gated.
  *
  * What is computed follows the GPTQ pages: "gptq" glossary page (Method and
  * Algorithm: layer-wise, Hessian from calibration data, quantize each weight
@@ -402,6 +405,177 @@ gptq_status_t gptq_quantize_layer_noalloc(const void* W, gptq_dtype_t wt,
  * set-up and returns GPTQ_OK.
  */
 gptq_status_t gptq_quantize_layer_noalloc_status(void* stream);
+
+/*
+ * ------------------------------------------------------------------------
+ * Running a solved layer on 8-bit integer tensor cores.
+ *
+ * A layer solved with one group per output row (group_size -1) is one
+ * integer matrix with a scale (and, asymmetric, a zero) for each output
+ * channel.  With the activations quantized to 8 bits by token the whole
+ * product is integer arithmetic with a scale for each token and channel.
+ * The pages describe only weight-only kernels for other hardware; these
+ * calls are this library's own and have no counterpart there.
+ *
+ *   gptq_layout_int8          the solver's packed codes as int8 rows
+ *   gptq_quantize_tokens      activations -> int8 tokens, a scale for each
+ *   gptq_norm_tokens          the norms before and after a block with its
+ *                             gate and residual scale; optionally straight
+ *                             to int8 tokens
+ *   gptq_matmul_int8          tokens x layer^T
+ *   gptq_matmul_int8_gated    act(tokens x gate^T) * (tokens x up^T)
+ *   gptq_int8_status          device-side status of the two products
+ *
+ * All take 0 <= tokens <= 67108864 (2^26) and 1 <= in <= 32768 (here also
+ * called d), work on the calling thread's current device, are asynchronous
+ * on stream, use no workspace, and keep no state between calls, so any
+ * number of them may overlap on any streams and be captured into graphs.
+ * tokens == 0 and out == 0 are no-ops.  Activations are [tokens][in], tokens
+ * in rows (the transpose of the Hessian's X).
+ */
+
+/* int8 tokens: q device int8 [tokens][in], 16-byte aligned, row stride ldq
+ * >= in, a multiple of 16; scale fp32[tokens]; sum int32[tokens], the sum of
+ * each token's codes.  Columns in .. ldq are neither read nor written. */
+typedef struct gptq_int8_tokens {
+  const int8_t* q;
+  int64_t ldq;
+  const float* scale;
+  const int32_t* sum;
+} gptq_int8_tokens_t;
+
+/* An int8 layer: w device int8 [out][in], 16-byte aligned, row stride ldw >=
+ * in, a multiple of 16; scale fp32[out]; zero int32[out] or NULL (all zero),
+ * |zero| <= 255.  The weight it stands for is scale[n] * (w[n][k] - zero[n]). */
+typedef struct gptq_int8_layer {
+  const int8_t* w;
+  int64_t ldw;
+  const float* scale;
+  const int32_t* zero;
+} gptq_int8_layer_t;
+
+typedef enum gptq_act {
+  GPTQ_ACT_SILU = 0,     /* g / (1 + exp(-g))                               */
+  GPTQ_ACT_GELU = 1,     /* g (1 + erf(g / sqrt 2)) / 2                      */
+  GPTQ_ACT_GELU_TANH = 2 /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2  */
+} gptq_act_t;
+
+typedef enum gptq_norm_kind {
+  GPTQ_NORM_RMS = 0,  /* v / sqrt(mean v^2 + eps) * weight + bias            */
+  GPTQ_NORM_LAYER = 1 /* (v - mean v) / sqrt(var v + eps) * weight + bias    */
+} gptq_norm_kind_t;
+
+/*
+ * int8 rows of a layer from the packed codes gptq_quantize_layer wrote with
+ * group_size -1 (qweight uint32 [out][in*bits/32], zeros int32[out], each in
+ * [0, 2^bits - 1]); the layer's scales are used as they are.
+ *   bits 8:       w = code - 128, zero = zeros - 128 (0 for a symmetric grid)
+ *   bits 2, 3, 4: w = code - zeros, zero = 0
+ * Outputs (device, caller-owned): w int8 [out][in], 16-byte aligned, row
+ * stride ldw >= in, a multiple of 16, columns in .. ldw not written; zero
+ * int32[out] or NULL (skipped).  Needs (in * bits) % 32 == 0
+ * (GPTQ_ERR_UNSUPPORTED otherwise).
+ */
+gptq_status_t gptq_layout_int8(const uint32_t* qweight, const int32_t* zeros,
+                               int64_t out, int64_t in, int bits, int8_t* w,
+                               int64_t ldw, int32_t* zero, void* stream);
+
+/*
+ * Quantize activations by token:
+ *   scale[t] = max_k |X[t][k]| / 127
+ *   q[t][k]  = clamp(rint(X[t][k] / scale[t]), -127, 127), 0 if scale[t] == 0
+ *   sum[t]   = sum_k q[t][k]
+ * the divisions and rint in IEEE float32 (round half to even), like the
+ * weight quantizer's.  A token that holds NaN or an infinity gets scale NaN
+ * and codes 0: its rows of a product come out NaN, the others are untouched.
+ * X: device [tokens][in] of type xt, row stride ldx >= in, any alignment of
+ * its type (16-byte aligned rows are read fastest).  Outputs as in
+ * gptq_int8_tokens_t.
+ */
+gptq_status_t gptq_quantize_tokens(const void* X, gptq_dtype_t xt,
+                                   int64_t tokens, int64_t in, int64_t ldx,
+                                   int8_t* q, int64_t ldq, float* scale,
+                                   int32_t* sum, void* stream);
+
+/*
+ * The norms around a block, with its gate and its residual scale:
+ *   u  = norm(y) with post_weight / post_bias     (post_weight NULL: u = y)
+ *   h' = alpha h + beta gate * u                  (gate NULL: 1; y NULL: u = 0)
+ *   x  = norm(h') with weight / bias              (weight NULL: no x)
+ *   q, scale, sum = gptq_quantize_tokens of x before it is rounded to yt
+ * In a pre-norm block y is the block's output, h the residual stream, x the
+ * next block's input; y = NULL is the first block's norm.  Statistics and all
+ * arithmetic are fp32; h' and x are rounded once, x being taken from h'
+ * before that rounding.
+ *   ht          type of h and h_out: yt or GPTQ_F32
+ *   yt          type of y, gate, weights, biases and x
+ *   gate        [d] with ldgate == 0, or [tokens][d] with ldgate >= d
+ *   h_out       NULL to skip; may be h itself (with ldh_out == ldh)
+ *   x           NULL to skip
+ *   q           NULL to skip, else with scale and sum
+ * All pointers are device pointers, aligned to their element (q: 16 bytes);
+ * outputs overlap neither inputs nor one another, but for h_out == h.
+ */
+typedef struct gptq_norm {
+  int64_t tokens, d;
+  gptq_dtype_t ht, yt;
+  gptq_norm_kind_t kind;
+  float eps, alpha, beta;
+  const void* h;
+  int64_t ldh;
+  const void* y;
+  int64_t ldy;
+  const void* post_weight;
+  const void* post_bias;
+  const void* gate;
+  int64_t ldgate;
+  const void* weight;
+  const void* bias;
+  void* h_out;
+  int64_t ldh_out;
+  void* x;
+  int64_t ldx;
+  int8_t* q;
+  int64_t ldq;
+  float* scale;
+  int32_t* sum;
+} gptq_norm_t;
+
+gptq_status_t gptq_norm_tokens(const gptq_norm_t* args, void* stream);
+
+/*
+ * Y[t][n] = x.scale[t] w.scale[n] (sum_k q[t][k] w[n][k]
+ *                                  - zero[n] x.sum[t]) + bias[n]
+ * The integer part is exact; it is converted to fp32 once, scaled and biased
+ * in fp32 and rounded once to yt.  The result does not depend on how the
+ * work is split.  bias: device fp32[out] or NULL.  Y: device [tokens][out] of
+ * type yt, row stride ldy >= out, any alignment of its type (16-byte aligned
+ * rows are written fastest), overlapping no input.  out <= 65535.
+ */
+gptq_status_t gptq_matmul_int8(const gptq_int8_tokens_t* x, int64_t tokens,
+                               int64_t in, const gptq_int8_layer_t* w,
+                               int64_t out, const float* bias, void* Y,
+                               gptq_dtype_t yt, int64_t ldy, void* stream);
+
+/*
+ * Y = act(G) * U with G and U the two products (without bias) of the tokens
+ * with gate and up, both out x in; activation and product in fp32, rounded
+ * once to yt.  One kernel: G and U exist in tensor memory only.
+ */
+gptq_status_t gptq_matmul_int8_gated(const gptq_int8_tokens_t* x,
+                                     int64_t tokens, int64_t in,
+                                     const gptq_int8_layer_t* gate,
+                                     const gptq_int8_layer_t* up, int64_t out,
+                                     gptq_act_t act, void* Y, gptq_dtype_t yt,
+                                     int64_t ldy, void* stream);
+
+/*
+ * Waits for stream and returns GPTQ_ERR_TIMEOUT if a bounded device-side wait
+ * in any int8 product on the current device has given up since the last such
+ * call (the products concerned are incomplete), else GPTQ_OK.  Clears the
+ * status.
+ */
+gptq_status_t gptq_int8_status(void* stream);
 
 #ifdef __cplusplus
 }

@@ -10,8 +10,9 @@ carry the C ABI's names (``include/gptq.h``):
     gptq_quantize_layer_noalloc(W, U, perm, dead, cfg, scales, zeros, g_idx, ...)
 
 plus ``solve_layer`` which allocates the outputs and workspace and makes the
-three calls in order.  If the shared library is missing the import fails: there
-is no fallback.
+three calls in order, and the calls that run a solved layer on 8-bit integer
+tensor cores (``serving.py``).  If the shared library is missing the import
+fails: there is no fallback.
 """
 from __future__ import annotations
 
@@ -28,6 +29,9 @@ __all__ = [
     "gptq_dequantize_layer", "gptq_export_checkpoint", "gptq_selftest_wait_timeout",
     "gptq_selftest_quotient",
     "solve_layer", "solve_block", "export_checkpoint", "STATUS_NAMES",
+    "gptq_layout_int8", "gptq_quantize_tokens", "gptq_norm_tokens", "gptq_matmul_int8",
+    "gptq_matmul_int8_gated", "gptq_int8_status", "Int8Layer", "Int8Tokens", "int8_layer",
+    "quantize_tokens", "norm_tokens", "linear_int8", "gated_int8", "mlp_int8",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgptq.so")
@@ -404,3 +408,14 @@ def solve_block(layers, activations=None, cfg=None, streams=True, hessians=None)
         s_layer = r.pop("stream")
         gptq_workspace_status(ws, s_layer)
     return results
+
+
+_SERVING = frozenset(__all__[__all__.index("gptq_layout_int8"):])
+
+
+def __getattr__(name):
+    """The serving calls, loaded with torch at their first use."""
+    if name in _SERVING:
+        from . import serving
+        return getattr(serving, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

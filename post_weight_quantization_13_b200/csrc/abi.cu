@@ -116,8 +116,6 @@ gptq_status_t hessian_accumulate(float* S, int64_t in, const void* X, gptq_dtype
   return GPTQ_OK;
 }
 
-namespace {
-
 gptq_status_t check_device() {
   const DeviceInfo& d = device_info();
   if (d.id < 0) return fail(GPTQ_ERR_CUDA, "no CUDA device is available");
@@ -126,6 +124,8 @@ gptq_status_t check_device() {
                 d.minor);
   return GPTQ_OK;
 }
+
+namespace {
 
 gptq_status_t check_ws(void* ws, size_t ws_bytes, size_t need) {
   if (!ws) return fail(GPTQ_ERR_WORKSPACE, "workspace pointer is NULL");

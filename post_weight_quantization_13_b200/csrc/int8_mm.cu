@@ -1,0 +1,477 @@
+// 8-bit integer products with a scale for each token and each channel:
+//
+//   y[t][n] = s_t s_n (sum_k q[t][k] w[n][k] - z_n sum_k q[t][k]) + b_n
+//
+// and the gated pair act(gate) * up of two such products over the same
+// tokens.  The sums are exact 32-bit integers (in <= 32768, so the largest is
+// below 1.7e9); one conversion to fp32, three fp32 operations and the output
+// conversion are the only roundings.
+//
+// split kernel: the weights' channels are the tensor core's 128 rows (tensor-
+// memory lanes), the tokens its columns (16 to 128), so a handful of tokens
+// still streams the weights through full-height MMAs.  The CTAs of a cluster
+// split k; their partial sums meet through distributed shared memory, where
+// each CTA adds and writes its share of the tokens.  Integer addition makes
+// the result independent of the split, and no workspace or atomic is needed.
+//   warp 0     TMA producer (one thread)
+//   warp 1     tensor memory, tcgen05.mma.kind::i8 (one thread)
+//   warps 2-5  tensor memory -> shared memory, cluster reduction, epilogue
+// Every wait is bounded; a wait that gives up raises ST_TIMEOUT in the
+// library's int8 status word, and the CTA drains and leaves.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cstring>
+#include <mutex>
+
+#include "gemm.cuh"
+#include "internal.cuh"
+
+namespace gptq {
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kBK = 128;                 // int8 elements of k per stage row (128-byte swizzle)
+constexpr int kTileM = 128;              // channels of a tile
+constexpr int kTileBytes = kTileM * kBK;
+constexpr int kMaxSplit = 8;             // portable cluster size
+
+// Raised by bounded waits that gave up, read and cleared by gptq_int8_status.
+__device__ uint32_t g_int8_status;
+
+struct MmParams {
+  const float* tscale;
+  const int32_t* tsum;
+  const float* wscale[2];  // [1]: the up projection of a gated pair
+  const int32_t* wzero[2];
+  const float* bias;
+  void* Y;
+  int64_t ldy;
+  int tokens, out, in;
+  int act;
+  int vec;  // rows of Y start on 16-byte boundaries
+  int ktiles, split, ntile, stages, stage_bytes, tmem_cols, ctiles;
+};
+
+struct SplitMaps {
+  CUtensorMap w[2];
+  CUtensorMap x;
+};
+
+// ----------------------------------------------------------------- pieces
+// D[tmem] (+)= A[smem] B[smem]^T, signed 8-bit inputs, 32-bit integers.
+__device__ __forceinline__ void umma_i8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor of kind::i8: 32-bit integer accumulator (bits 4-5 =
+// 2), both operands signed (bits 7-9 and 10-12 = 1) and K-major, N >> 3 at
+// bits 17-22, M >> 4 at bits 24-28.
+__host__ __device__ constexpr uint32_t idesc_i8(uint32_t M, uint32_t N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ int4 ld_cluster_int4(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// The gate's activation in fp32.  tanh's gelu is written through the logistic
+// function, 0.5 (1 + tanh z) = 1 / (1 + exp(-2 z)), so both need one
+// exponential and one quotient (__expf and __fdividef: a few units in the
+// last place of fp32).
+__device__ __forceinline__ float activate(float g, int act) {
+  if (act == GPTQ_ACT_GELU) return 0.5f * g * (1.f + erff(g * 0.70710678118654752f));
+  const float z = act == GPTQ_ACT_SILU ? g : 1.5957691216057308f * fmaf(0.044715f * g * g, g, g);
+  return __fdividef(g, 1.f + __expf(-z));
+}
+
+__device__ __forceinline__ float scaled(int acc, int zero, int tsum, float tscale, float wscale) {
+  return (float)(acc - zero * tsum) * tscale * wscale;
+}
+
+// ------------------------------------------------------------ split kernel
+template <int G, typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    int8_split_kernel(const __grid_constant__ SplitMaps maps, const __grid_constant__ MmParams kp) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint64_t* full = (uint64_t*)(smem + (size_t)kp.stages * kp.stage_bytes);
+  uint64_t* empty = full + kp.stages;
+  uint64_t* acc_full = empty + kp.stages;
+  uint64_t* drain = acc_full + 1;
+  uint32_t* tmem_slot = (uint32_t*)(drain + 1);
+  volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int split = kp.split;
+  const int rank = split > 1 ? (int)cluster_rank() : 0;
+  const int tile = (int)blockIdx.x / split;
+  const int n0 = (tile % kp.ctiles) * kTileM;
+  const int t0 = (tile / kp.ctiles) * kp.ntile;
+  const int kt0 = (int)((int64_t)kp.ktiles * rank / split), kt1 = (int)((int64_t)kp.ktiles * (rank + 1) / split);
+  const int ntile = kp.ntile;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kp.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, (uint32_t)kp.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const int stages = kp.stages, stage_bytes = kp.stage_bytes;
+      const uint32_t bytes = (uint32_t)(G * kTileBytes + ntile * kBK);
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int kt = kt0; kt < kt1; ++kt) {
+        if (!mbar_wait(&empty[stage], phase ^ 1)) {
+          raise_status(&g_int8_status, ST_TIMEOUT);
+          *abort_flag = 1;
+        }
+        if (*abort_flag) break;
+        uint8_t* sb = smem + (size_t)stage * stage_bytes;
+        mbar_arrive_expect_tx(&full[stage], bytes);
+#pragma unroll
+        for (int g = 0; g < G; ++g) tma_load_2d(sb + g * kTileBytes, &maps.w[g], &full[stage], kt * kBK, n0);
+        tma_load_2d(sb + G * kTileBytes, &maps.x, &full[stage], kt * kBK, t0);
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const int stages = kp.stages, stage_bytes = kp.stage_bytes;
+      const uint32_t idesc = idesc_i8(kTileM, (uint32_t)ntile);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int kt = kt0; kt < kt1; ++kt) {
+        if (!mbar_wait(&full[stage], phase)) {
+          raise_status(&g_int8_status, ST_TIMEOUT);
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sb = smem_u32(smem + (size_t)stage * stage_bytes);
+        const uint32_t xb = sb + G * kTileBytes;
+#pragma unroll
+        for (int kk = 0; kk < kBK / 32; ++kk)
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+            umma_i8(tbase + (uint32_t)(g * ntile), smem_desc_k_sw128(sb + g * kTileBytes + kk * 32),
+                    smem_desc_k_sw128(xb + kk * 32), idesc, (kt > kt0 || kk > 0) ? 1u : 0u);
+        umma_commit(&empty[stage]);
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (ok) umma_commit(acc_full);
+    }
+  } else {
+    // partial sums -> shared memory, [g][token][channel]; the pipeline's
+    // stages are free once the accumulators are complete
+    const int quarter = warp & 3;
+    if (!mbar_wait_sleep(acc_full, 0)) {
+      raise_status(&g_int8_status, ST_TIMEOUT);
+      *abort_flag = 1;
+    } else {
+      tc_fence_after();
+      int* part = (int*)smem;
+      const int c = quarter * 32 + lane;
+      for (int j0 = 0; j0 < G * ntile; j0 += 16) {
+        float v[16];
+        tmem_ld16(tbase + (uint32_t)j0 + ((uint32_t)(quarter * 32) << 16), v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(j0 + j) * kTileM + c] = __float_as_int(v[j]);
+      }
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  // every CTA's partial sums are in place (a CTA whose wait gave up arrives too)
+  if (split > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  if (warp >= 2) {
+    // rank r finishes tokens [ntile r / split, ntile (r + 1) / split): one
+    // token a warp, four channels a lane
+    const int j0 = ntile * rank / split, j1 = ntile * (rank + 1) / split;
+    const int n = n0 + 4 * lane;
+    const uint32_t part = smem_u32(smem);
+    float ws[G][4];
+    int wz[G][4];
+    float bias[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool in = n + i < kp.out;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        ws[g][i] = in ? __ldg(kp.wscale[g] + n + i) : 0.f;
+        wz[g][i] = in && kp.wzero[g] ? __ldg(kp.wzero[g] + n + i) : 0;
+      }
+      bias[i] = G == 1 && in && kp.bias ? __ldg(kp.bias + n + i) : 0.f;
+    }
+    for (int j = j0 + warp - 2; j < j1; j += 4) {
+      const int t = t0 + j;
+      if (t >= kp.tokens) break;
+      const float ts = __ldg(kp.tscale + t);
+      const int sum = __ldg(kp.tsum + t);
+      int acc[G][4];
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const uint32_t at = part + (uint32_t)(((g * ntile + j) * kTileM + 4 * lane) * 4);
+        int4 a = make_int4(0, 0, 0, 0);
+        for (int r = 0; r < split; ++r) {
+          const int4 b = split > 1 ? ld_cluster_int4(map_to_rank(at, (uint32_t)r))
+                                   : *reinterpret_cast<const int4*>(smem + (at - part));
+          a.x += b.x;
+          a.y += b.y;
+          a.z += b.z;
+          a.w += b.w;
+        }
+        acc[g][0] = a.x;
+        acc[g][1] = a.y;
+        acc[g][2] = a.z;
+        acc[g][3] = a.w;
+      }
+      alignas(16) T o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float y = scaled(acc[0][i], wz[0][i], sum, ts, ws[0][i]);
+        if (G == 2)
+          y = activate(y, kp.act) * scaled(acc[G - 1][i], wz[G - 1][i], sum, ts, ws[G - 1][i]);
+        else
+          y += bias[i];
+        o[i] = from_f32<T>(y);
+      }
+      T* dst = (T*)kp.Y + (int64_t)t * kp.ldy + n;
+      if (kp.vec && n + 4 <= kp.out) {
+        if (sizeof(T) == 2)
+          *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(o);
+        else
+          *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(o);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + i < kp.out) dst[i] = o[i];
+      }
+    }
+  }
+  __syncwarp();
+  // no CTA leaves while a peer still reads its partial sums
+  if (split > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  if (*abort_flag) {
+    // let copies and MMAs already issued finish before the memory goes away
+    if (threadIdx.x == 32) {
+      umma_commit(drain);
+      mbar_wait(drain, 0);
+    }
+    if (threadIdx.x == 0) {
+      const uint64_t start = globaltimer();
+      while (globaltimer() - start < 1000000ull) {
+      }
+    }
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tbase, (uint32_t)kp.tmem_cols);
+  }
+}
+
+// ------------------------------------------------------------------- host
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = (EncodeTiledFn)p;
+  });
+  return fn;
+}
+
+// A K-major int8 operand (rows x in, row stride ld bytes) in boxes of
+// box_rows rows by 128 bytes; what lies past the matrix reads as zero.
+bool int8_map(CUtensorMap* m, const int8_t* base, int64_t rows, int64_t in, int64_t ld, int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t gdim[2] = {(cuuint64_t)in, (cuuint64_t)rows};
+  cuuint64_t gstride[1] = {(cuuint64_t)ld};
+  cuuint32_t box[2] = {(cuuint32_t)kBK, (cuuint32_t)box_rows};
+  cuuint32_t estride[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(base), gdim, gstride, box, estride,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int G, typename T>
+cudaError_t launch_split(const SplitMaps& maps, const MmParams& kp, int64_t tiles, cudaStream_t st) {
+  const void* f = (const void*)int8_split_kernel<G, T>;
+  cudaError_t e = ensure_smem_limit(f, 232448);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * kp.split));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = 1024 + (size_t)kp.stages * kp.stage_bytes + 256;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)kp.split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kp.split > 1 ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, int8_split_kernel<G, T>, maps, kp);
+  note_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Tiles of 128 channels by up to 128 tokens; k is split over 2, 4 or 8 CTAs
+// while the tiles leave SMs idle and every CTA keeps at least two k-tiles.
+template <int G>
+cudaError_t run_split(MmParams kp, const gptq_int8_tokens_t* x, const gptq_int8_layer_t* const (&w)[2],
+                      gptq_dtype_t yt, cudaStream_t st, int sms) {
+  kp.ntile = std::min(128, (kp.tokens + 15) / 16 * 16);
+  kp.ctiles = (kp.out + kTileM - 1) / kTileM;
+  kp.ktiles = (kp.in + kBK - 1) / kBK;
+  const int64_t tiles = (int64_t)kp.ctiles * ((kp.tokens + kp.ntile - 1) / kp.ntile);
+  kp.split = 1;
+  while (kp.split < kMaxSplit && tiles * kp.split * 2 <= sms && kp.ktiles >= kp.split * 4) kp.split *= 2;
+  kp.stage_bytes = G * kTileBytes + kp.ntile * kBK;
+  kp.tmem_cols = 32;
+  while (kp.tmem_cols < G * kp.ntile) kp.tmem_cols *= 2;
+  // The stages fill shared memory, so no two CTAs of these kernels share an
+  // SM: a CTA that waits for tensor memory held by another could otherwise
+  // hold up that one's cluster.
+  kp.stages = (232448 - 1024 - 256) / kp.stage_bytes;
+  if (kp.stages > 12) kp.stages = 12;
+  SplitMaps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  for (int g = 0; g < G; ++g)
+    if (!int8_map(&maps.w[g], w[g]->w, kp.out, kp.in, w[g]->ldw, kTileM)) return cudaErrorInvalidValue;
+  if (!int8_map(&maps.x, x->q, kp.tokens, kp.in, x->ldq, kp.ntile)) return cudaErrorInvalidValue;
+  switch (yt) {
+    case GPTQ_F16:
+      return launch_split<G, __half>(maps, kp, tiles, st);
+    case GPTQ_BF16:
+      return launch_split<G, __nv_bfloat16>(maps, kp, tiles, st);
+    default:
+      return launch_split<G, float>(maps, kp, tiles, st);
+  }
+}
+
+template <int G>
+cudaError_t run(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const gptq_int8_layer_t* const (&w)[2],
+                int64_t out, const float* bias, int act, void* Y, gptq_dtype_t yt, int64_t ldy, cudaStream_t st) {
+  MmParams kp = {};
+  kp.tscale = x->scale;
+  kp.tsum = x->sum;
+  for (int g = 0; g < G; ++g) {
+    kp.wscale[g] = w[g]->scale;
+    kp.wzero[g] = w[g]->zero;
+  }
+  kp.bias = bias;
+  kp.Y = Y;
+  kp.ldy = ldy;
+  kp.tokens = (int)tokens;
+  kp.out = (int)out;
+  kp.in = (int)in;
+  kp.act = act;
+  kp.vec = (uintptr_t)Y % 16 == 0 && (ldy * (yt == GPTQ_F32 ? 4 : 2)) % 16 == 0;
+  return run_split<G>(kp, x, w, yt, st, device_info().sms);
+}
+
+}  // namespace
+
+gptq_status_t matmul_int8(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const gptq_int8_layer_t* w,
+                          int64_t out, const float* bias, void* Y, gptq_dtype_t yt, int64_t ldy, cudaStream_t st) {
+  const gptq_int8_layer_t* const ws[2] = {w, nullptr};
+  CUDA_TRY(run<1>(x, tokens, in, ws, out, bias, 0, Y, yt, ldy, st));
+  return GPTQ_OK;
+}
+
+gptq_status_t matmul_int8_gated(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const gptq_int8_layer_t* gate,
+                                const gptq_int8_layer_t* up, int64_t out, int act, void* Y, gptq_dtype_t yt,
+                                int64_t ldy, cudaStream_t st) {
+  const gptq_int8_layer_t* const ws[2] = {gate, up};
+  CUDA_TRY(run<2>(x, tokens, in, ws, out, nullptr, act, Y, yt, ldy, st));
+  return GPTQ_OK;
+}
+
+gptq_status_t int8_status(cudaStream_t st) {
+  uint32_t status = 0;
+  void* at = nullptr;
+  CUDA_TRY(cudaGetSymbolAddress(&at, g_int8_status));
+  CUDA_TRY(cudaMemcpyAsync(&status, at, sizeof(status), cudaMemcpyDeviceToHost, st));
+  CUDA_TRY(cudaMemsetAsync(at, 0, sizeof(status), st));
+  CUDA_TRY(cudaStreamSynchronize(st));
+  if (status & ST_TIMEOUT) return fail(GPTQ_ERR_TIMEOUT, "a bounded device-side wait gave up in an int8 product");
+  return GPTQ_OK;
+}
+
+}  // namespace gptq

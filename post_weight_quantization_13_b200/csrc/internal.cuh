@@ -70,6 +70,23 @@ gptq_status_t export_checkpoint(const uint32_t* qweight, const float* scales, co
 gptq_status_t hessian_accumulate(float* S, int64_t in, const void* X, gptq_dtype_t xt, int64_t tokens, int64_t ldx,
                                  cudaStream_t st);
 
+// GPTQ_OK when the current device is one this library is built for.
+gptq_status_t check_device();
+
+// The 8-bit serving path (tokens.cu, int8_mm.cu); arguments checked in
+// abi_int8.cu.
+gptq_status_t layout_int8(const uint32_t* qweight, const int32_t* zeros, int64_t out, int64_t in, int bits, int8_t* w,
+                          int64_t ldw, int32_t* zero, cudaStream_t st);
+gptq_status_t quantize_tokens(const void* X, gptq_dtype_t xt, int64_t tokens, int64_t in, int64_t ldx, int8_t* q,
+                              int64_t ldq, float* scale, int32_t* sum, cudaStream_t st);
+gptq_status_t norm_tokens(const gptq_norm_t* a, cudaStream_t st);
+gptq_status_t matmul_int8(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const gptq_int8_layer_t* w,
+                          int64_t out, const float* bias, void* Y, gptq_dtype_t yt, int64_t ldy, cudaStream_t st);
+gptq_status_t matmul_int8_gated(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const gptq_int8_layer_t* gate,
+                                const gptq_int8_layer_t* up, int64_t out, int act, void* Y, gptq_dtype_t yt,
+                                int64_t ldy, cudaStream_t st);
+gptq_status_t int8_status(cudaStream_t st);
+
 // Blocked Cholesky R = L L^T of the np x np matrix R (lower triangle, np a
 // multiple of 128) and the inverse M = L^-1, in one cooperative launch
 // (chol.cu).  Outputs, split (tf32 hi + exact remainder): the panel tiles of L
