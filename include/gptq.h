@@ -424,12 +424,13 @@ gptq_status_t gptq_quantize_layer_noalloc_status(void* stream);
  *                             to int8 tokens
  *   gptq_matmul_int8          tokens x layer^T
  *   gptq_matmul_int8_gated    act(tokens x gate^T) * (tokens x up^T)
+ *   gptq_linear_int8(_gated)  the same from floating activations
  *   gptq_int8_status          device-side status of the two products
  *
  * All take 0 <= tokens <= 67108864 (2^26) and 1 <= in <= 32768 (here also
  * called d), work on the calling thread's current device, are asynchronous
- * on stream, use no workspace, and keep no state between calls, so any
- * number of them may overlap on any streams and be captured into graphs.
+ * on stream and keep no state between calls, so any number of them may
+ * overlap on any streams and be captured into graphs.
  * tokens == 0 and out == 0 are no-ops.  Activations are [tokens][in], tokens
  * in rows (the transpose of the Hessian's X).
  */
@@ -482,11 +483,11 @@ gptq_status_t gptq_layout_int8(const uint32_t* qweight, const int32_t* zeros,
 
 /*
  * Quantize activations by token:
- *   scale[t] = max_k |X[t][k]| / 127
+ *   scale[t] = max_k |X[t][k]| * (1/127), the constant rounded to float32
  *   q[t][k]  = clamp(rint(X[t][k] / scale[t]), -127, 127), 0 if scale[t] == 0
  *   sum[t]   = sum_k q[t][k]
- * the divisions and rint in IEEE float32 (round half to even), like the
- * weight quantizer's.  A token that holds NaN or an infinity gets scale NaN
+ * the product, the division and rint in IEEE float32 (round half to even),
+ * like the weight quantizer's.  A token that holds NaN or an infinity gets scale NaN
  * and codes 0: its rows of a product come out NaN, the others are untouched.
  * X: device [tokens][in] of type xt, row stride ldx >= in, any alignment of
  * its type (16-byte aligned rows are read fastest).  Outputs as in
@@ -568,6 +569,31 @@ gptq_status_t gptq_matmul_int8_gated(const gptq_int8_tokens_t* x,
                                      const gptq_int8_layer_t* up, int64_t out,
                                      gptq_act_t act, void* Y, gptq_dtype_t yt,
                                      int64_t ldy, void* stream);
+
+/*
+ * gptq_quantize_tokens followed by gptq_matmul_int8 (or _gated), bit for bit,
+ * on floating activations X [tokens][in] of type xt, row stride ldx.  The
+ * tokens' codes live in the workspace ws of ws_bytes >=
+ * gptq_linear_int8_ws_bytes(tokens, in), 256-byte aligned, which needs no
+ * initialisation and must not be used by two calls at once; for a few tokens
+ * that size is 0 (one kernel does both, ws may be NULL).
+ */
+size_t gptq_linear_int8_ws_bytes(int64_t tokens, int64_t in);
+
+gptq_status_t gptq_linear_int8(const void* X, gptq_dtype_t xt, int64_t tokens,
+                               int64_t in, int64_t ldx,
+                               const gptq_int8_layer_t* w, int64_t out,
+                               const float* bias, void* Y, gptq_dtype_t yt,
+                               int64_t ldy, void* ws, size_t ws_bytes,
+                               void* stream);
+
+gptq_status_t gptq_linear_int8_gated(const void* X, gptq_dtype_t xt,
+                                     int64_t tokens, int64_t in, int64_t ldx,
+                                     const gptq_int8_layer_t* gate,
+                                     const gptq_int8_layer_t* up, int64_t out,
+                                     gptq_act_t act, void* Y, gptq_dtype_t yt,
+                                     int64_t ldy, void* ws, size_t ws_bytes,
+                                     void* stream);
 
 /*
  * Waits for stream and returns GPTQ_ERR_TIMEOUT if a bounded device-side wait

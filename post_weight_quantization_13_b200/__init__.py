@@ -30,7 +30,8 @@ __all__ = [
     "gptq_selftest_quotient",
     "solve_layer", "solve_block", "export_checkpoint", "STATUS_NAMES",
     "gptq_layout_int8", "gptq_quantize_tokens", "gptq_norm_tokens", "gptq_matmul_int8",
-    "gptq_matmul_int8_gated", "gptq_int8_status", "Int8Layer", "Int8Tokens", "int8_layer",
+    "gptq_matmul_int8_gated", "gptq_linear_int8", "gptq_linear_int8_gated",
+    "gptq_linear_int8_ws_bytes", "gptq_int8_status", "Int8Layer", "Int8Tokens", "int8_layer",
     "quantize_tokens", "norm_tokens", "linear_int8", "gated_int8", "mlp_int8",
 ]
 

@@ -125,8 +125,6 @@ gptq_status_t check_device() {
   return GPTQ_OK;
 }
 
-namespace {
-
 gptq_status_t check_ws(void* ws, size_t ws_bytes, size_t need) {
   if (!ws) return fail(GPTQ_ERR_WORKSPACE, "workspace pointer is NULL");
   if (((uintptr_t)ws & 255u) != 0) return fail(GPTQ_ERR_WORKSPACE, "workspace is not 256-byte aligned");
@@ -134,6 +132,8 @@ gptq_status_t check_ws(void* ws, size_t ws_bytes, size_t need) {
     return fail(GPTQ_ERR_WORKSPACE, "workspace too small: %zu bytes given, %zu needed", ws_bytes, need);
   return GPTQ_OK;
 }
+
+namespace {
 
 bool dtype_ok(gptq_dtype_t t) { return t == GPTQ_F16 || t == GPTQ_BF16 || t == GPTQ_F32; }
 

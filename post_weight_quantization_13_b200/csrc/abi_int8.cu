@@ -193,6 +193,48 @@ gptq_status_t gptq_matmul_int8_gated(const gptq_int8_tokens_t* x, int64_t tokens
   return matmul_int8_gated(x, tokens, in, gate, up, out, (int)act, Y, yt, ldy, (cudaStream_t)stream);
 }
 
+size_t gptq_linear_int8_ws_bytes(int64_t tokens, int64_t in) {
+  if (tokens < 0 || tokens > kMaxTokens || in < 1 || in > kMaxIn) return 0;
+  return linear_int8_ws_bytes(tokens, in);
+}
+
+gptq_status_t gptq_linear_int8(const void* X, gptq_dtype_t xt, int64_t tokens, int64_t in, int64_t ldx,
+                               const gptq_int8_layer_t* w, int64_t out, const float* bias, void* Y, gptq_dtype_t yt,
+                               int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+  clear_error();
+  TRY(check_sizes(tokens, in, out));
+  if (!dtype_ok(xt) || !dtype_ok(yt)) return fail(GPTQ_ERR_INVALID_ARG, "unknown dtype (X %d, Y %d)", (int)xt, (int)yt);
+  if (tokens == 0 || out == 0) return GPTQ_OK;
+  TRY(check_rows("X", X, ldx, in, xt));
+  TRY(check_layer("w", w, in));
+  if (bias) TRY(check_vector("bias", bias, 4));
+  TRY(check_rows("Y", Y, ldy, out, yt));
+  const size_t need = linear_int8_ws_bytes(tokens, in);
+  if (need) TRY(check_ws(ws, ws_bytes, need));
+  TRY(check_device());
+  return linear_int8(X, xt, tokens, in, ldx, w, nullptr, out, bias, 0, Y, yt, ldy, ws, (cudaStream_t)stream);
+}
+
+gptq_status_t gptq_linear_int8_gated(const void* X, gptq_dtype_t xt, int64_t tokens, int64_t in, int64_t ldx,
+                                     const gptq_int8_layer_t* gate, const gptq_int8_layer_t* up, int64_t out,
+                                     gptq_act_t act, void* Y, gptq_dtype_t yt, int64_t ldy, void* ws, size_t ws_bytes,
+                                     void* stream) {
+  clear_error();
+  TRY(check_sizes(tokens, in, out));
+  if (!dtype_ok(xt) || !dtype_ok(yt)) return fail(GPTQ_ERR_INVALID_ARG, "unknown dtype (X %d, Y %d)", (int)xt, (int)yt);
+  if (act != GPTQ_ACT_SILU && act != GPTQ_ACT_GELU && act != GPTQ_ACT_GELU_TANH)
+    return fail(GPTQ_ERR_INVALID_ARG, "unknown activation %d", (int)act);
+  if (tokens == 0 || out == 0) return GPTQ_OK;
+  TRY(check_rows("X", X, ldx, in, xt));
+  TRY(check_layer("gate", gate, in));
+  TRY(check_layer("up", up, in));
+  TRY(check_rows("Y", Y, ldy, out, yt));
+  const size_t need = linear_int8_ws_bytes(tokens, in);
+  if (need) TRY(check_ws(ws, ws_bytes, need));
+  TRY(check_device());
+  return linear_int8(X, xt, tokens, in, ldx, gate, up, out, nullptr, (int)act, Y, yt, ldy, ws, (cudaStream_t)stream);
+}
+
 gptq_status_t gptq_int8_status(void* stream) {
   clear_error();
   TRY(check_device());

@@ -26,6 +26,7 @@
 #include <mutex>
 
 #include "gemm.cuh"
+#include "int8.cuh"
 #include "internal.cuh"
 
 namespace gptq {
@@ -96,29 +97,6 @@ __device__ __forceinline__ int4 ld_cluster_int4(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
-}
-
-template <typename T>
-__device__ __forceinline__ T from_f32(float x);
-template <>
-__device__ __forceinline__ float from_f32<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-
-// The gate's activation in fp32.  tanh's gelu is written through the logistic
-// function, 0.5 (1 + tanh z) = 1 / (1 + exp(-2 z)), so both need one
-// exponential and one quotient (__expf and __fdividef: a few units in the
-// last place of fp32).
-__device__ __forceinline__ float activate(float g, int act) {
-  if (act == GPTQ_ACT_GELU) return 0.5f * g * (1.f + erff(g * 0.70710678118654752f));
-  const float z = act == GPTQ_ACT_SILU ? g : 1.5957691216057308f * fmaf(0.044715f * g * g, g, g);
-  return __fdividef(g, 1.f + __expf(-z));
-}
-
-__device__ __forceinline__ float scaled(int acc, int zero, int tsum, float tscale, float wscale) {
-  return (float)(acc - zero * tsum) * tscale * wscale;
 }
 
 // ------------------------------------------------------------ split kernel
@@ -446,12 +424,33 @@ cudaError_t run(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const g
   return run_split<G>(kp, x, w, yt, st, device_info().sms);
 }
 
+// Whether the rows kernel (int8_rows.cu) takes a product.
+bool few(int64_t tokens) { return tokens <= 4; }
+
+cudaError_t multiply(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const gptq_int8_layer_t* const (&w)[2],
+                     int64_t out, const float* bias, int act, void* Y, gptq_dtype_t yt, int64_t ldy, cudaStream_t st) {
+  if (few(tokens)) return rows_int8(nullptr, 0, 0, x, tokens, in, w, out, bias, act, Y, yt, ldy, st);
+  if (w[1]) return run<2>(x, tokens, in, w, out, bias, act, Y, yt, ldy, st);
+  return run<1>(x, tokens, in, w, out, bias, act, Y, yt, ldy, st);
+}
+
+// The workspace of a product that quantizes its tokens: codes, scales, sums.
+struct TokenScratch {
+  gptq_int8_tokens_t x;
+  size_t bytes;
+  TokenScratch(void* ws, int64_t tokens, int64_t in) {
+    const int64_t ldq = round_up(in, 16), codes = round_up(tokens * ldq, 256), vec = round_up(tokens * 4, 256);
+    x = {(const int8_t*)ws, ldq, (const float*)((uintptr_t)ws + codes), (const int32_t*)((uintptr_t)ws + codes + vec)};
+    bytes = (size_t)(codes + 2 * vec);
+  }
+};
+
 }  // namespace
 
 gptq_status_t matmul_int8(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const gptq_int8_layer_t* w,
                           int64_t out, const float* bias, void* Y, gptq_dtype_t yt, int64_t ldy, cudaStream_t st) {
   const gptq_int8_layer_t* const ws[2] = {w, nullptr};
-  CUDA_TRY(run<1>(x, tokens, in, ws, out, bias, 0, Y, yt, ldy, st));
+  CUDA_TRY(multiply(x, tokens, in, ws, out, bias, 0, Y, yt, ldy, st));
   return GPTQ_OK;
 }
 
@@ -459,7 +458,27 @@ gptq_status_t matmul_int8_gated(const gptq_int8_tokens_t* x, int64_t tokens, int
                                 const gptq_int8_layer_t* up, int64_t out, int act, void* Y, gptq_dtype_t yt,
                                 int64_t ldy, cudaStream_t st) {
   const gptq_int8_layer_t* const ws[2] = {gate, up};
-  CUDA_TRY(run<2>(x, tokens, in, ws, out, nullptr, act, Y, yt, ldy, st));
+  CUDA_TRY(multiply(x, tokens, in, ws, out, nullptr, act, Y, yt, ldy, st));
+  return GPTQ_OK;
+}
+
+size_t linear_int8_ws_bytes(int64_t tokens, int64_t in) {
+  return few(tokens) ? 0 : TokenScratch(nullptr, tokens, in).bytes;
+}
+
+gptq_status_t linear_int8(const void* X, gptq_dtype_t xt, int64_t tokens, int64_t in, int64_t ldx,
+                          const gptq_int8_layer_t* w, const gptq_int8_layer_t* up, int64_t out, const float* bias,
+                          int act, void* Y, gptq_dtype_t yt, int64_t ldy, void* ws, cudaStream_t st) {
+  const gptq_int8_layer_t* const layers[2] = {w, up};
+  if (few(tokens)) {
+    CUDA_TRY(rows_int8(X, xt, ldx, nullptr, tokens, in, layers, out, bias, act, Y, yt, ldy, st));
+    return GPTQ_OK;
+  }
+  const TokenScratch q(ws, tokens, in);
+  const gptq_status_t s = quantize_tokens(X, xt, tokens, in, ldx, const_cast<int8_t*>(q.x.q), q.x.ldq,
+                                          const_cast<float*>(q.x.scale), const_cast<int32_t*>(q.x.sum), st);
+  if (s != GPTQ_OK) return s;
+  CUDA_TRY(multiply(&q.x, tokens, in, layers, out, bias, act, Y, yt, ldy, st));
   return GPTQ_OK;
 }
 

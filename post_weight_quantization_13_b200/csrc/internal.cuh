@@ -85,7 +85,19 @@ gptq_status_t matmul_int8(const gptq_int8_tokens_t* x, int64_t tokens, int64_t i
 gptq_status_t matmul_int8_gated(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const gptq_int8_layer_t* gate,
                                 const gptq_int8_layer_t* up, int64_t out, int act, void* Y, gptq_dtype_t yt,
                                 int64_t ldy, cudaStream_t st);
+// The two with their tokens quantized on the way (up == nullptr: plain); ws
+// holds linear_int8_ws_bytes, 256-byte aligned.
+size_t linear_int8_ws_bytes(int64_t tokens, int64_t in);
+gptq_status_t linear_int8(const void* X, gptq_dtype_t xt, int64_t tokens, int64_t in, int64_t ldx,
+                          const gptq_int8_layer_t* w, const gptq_int8_layer_t* up, int64_t out, const float* bias,
+                          int act, void* Y, gptq_dtype_t yt, int64_t ldy, void* ws, cudaStream_t st);
+// Both for at most four tokens (int8_rows.cu): tokens8, or x of type xt.
+cudaError_t rows_int8(const void* x, int xt, int64_t ldx, const gptq_int8_tokens_t* tokens8, int64_t tokens, int64_t in,
+                      const gptq_int8_layer_t* const (&w)[2], int64_t out, const float* bias, int act, void* Y,
+                      gptq_dtype_t yt, int64_t ldy, cudaStream_t st);
 gptq_status_t int8_status(cudaStream_t st);
+// Checks of a workspace argument (abi.cu).
+gptq_status_t check_ws(void* ws, size_t ws_bytes, size_t need);
 
 // Blocked Cholesky R = L L^T of the np x np matrix R (lower triangle, np a
 // multiple of 128) and the inverse M = L^-1, in one cooperative launch

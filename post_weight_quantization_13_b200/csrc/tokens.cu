@@ -16,63 +16,11 @@
 #include <algorithm>
 
 #include "gemm.cuh"
+#include "int8.cuh"
 #include "internal.cuh"
 
 namespace gptq {
 namespace {
-
-// ------------------------------------------------------------ element access
-template <typename T>
-__device__ __forceinline__ float to_f32(T x);
-template <>
-__device__ __forceinline__ float to_f32<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_f32<__half>(__half x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename T>
-__device__ __forceinline__ T from_f32(float x);
-template <>
-__device__ __forceinline__ float from_f32<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-
-// Eight consecutive elements as loaded; left elements (>= 1) lie inside the
-// row, those past its end read as zero.  vec: the address is 16-byte aligned.
-template <typename T>
-struct Raw8 {
-  alignas(16) T v[8];
-};
-template <typename T>
-__device__ __forceinline__ Raw8<T> load8(const T* __restrict__ p, int left, bool vec) {
-  Raw8<T> r;
-  if (vec && left >= 8) {
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-      reinterpret_cast<uint4*>(r.v)[i] = reinterpret_cast<const uint4*>(p)[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r.v[i] = i < left ? p[i] : from_f32<T>(0.f);
-  }
-  return r;
-}
-template <typename T>
-__device__ __forceinline__ void store8(T* __restrict__ p, const float* v, int left, bool vec) {
-  Raw8<T> r;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) r.v[i] = from_f32<T>(v[i]);
-  if (vec && left >= 8) {
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-      reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(r.v)[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < left) p[i] = r.v[i];
-  }
-}
 
 // ------------------------------------------------------------ row reductions
 // Reductions over the threads of one row (blockDim.x of them).  Successive
@@ -110,14 +58,9 @@ struct RowReduce {
   }
 };
 
-// The token quantizer on a row in registers: s = RN32(max |x| / 127), q =
-// clamp(rint(RN32(x / s)), -127, 127), both roundings IEEE like the weight
-// quantizer's.  The largest magnitude is taken on the bit patterns, where
+// The token quantizer on a row in registers (TokenScale holds its arithmetic).  The largest magnitude is taken on the bit patterns, where
 // NaN and infinity sort above every finite value; such a row gets s = NaN and
-// codes of zero, so its product row is NaN and no other row is touched.  The
-// quotient comes from quot_rn (five operations instead of a divide) while s
-// is in its range; an x too small for that range has |x / s| < 1/2 either
-// way, its code is 0.
+// codes of zero, so its product row is NaN and no other row is touched.
 template <int NV>
 __device__ __forceinline__ void quantize_row(const float (&v)[NV][8], int d, RowReduce& red, int8_t* __restrict__ q,
                                              float* __restrict__ scale, int32_t* __restrict__ sum) {
@@ -127,11 +70,7 @@ __device__ __forceinline__ void quantize_row(const float (&v)[NV][8], int d, Row
 #pragma unroll
     for (int u = 0; u < 8; ++u) top = max(top, __float_as_uint(v[i][u]) & 0x7fffffffu);
   top = red.max_u32(top);
-  const bool finite = top < 0x7f800000u;
-  const float s = finite ? __fdiv_rn(__uint_as_float(top), 127.f) : __uint_as_float(0x7fc00000u);
-  const bool some = finite && s > 0.f;
-  const bool fast = s >= 0x1p-60f && s <= 0x1p60f;
-  const float inv = fast ? __frcp_rn(s) : 0.f;
+  const TokenScale s(top);
   int total = 0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -140,12 +79,7 @@ __device__ __forceinline__ void quantize_row(const float (&v)[NV][8], int d, Row
     uint32_t w[2] = {0u, 0u};
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      int code = 0;
-      if (some) {
-        const float x = v[i][u];
-        code = __float2int_rn(fast ? quot_rn(x, s, inv) : __fdiv_rn(x, s));
-        code = min(127, max(-127, code));
-      }
+      const int code = s.code(v[i][u]);
       total += code;
       w[u >> 2] |= (uint32_t)(code & 0xff) << (8 * (u & 3));
     }
@@ -159,7 +93,7 @@ __device__ __forceinline__ void quantize_row(const float (&v)[NV][8], int d, Row
   }
   total = red.sum_s32(total);
   if (threadIdx.x == 0) {
-    *scale = s;
+    *scale = s.scale;
     *sum = total;
   }
 }

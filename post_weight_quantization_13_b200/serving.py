@@ -21,7 +21,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import _check, _dt, _i64, _p, _ptr, _rowmajor, _stream, lib
+from . import _check, _i64, _p, _stream, lib
 
 _NORMS = {"rms": 0, "layer": 1}
 _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
@@ -56,6 +56,14 @@ lib.gptq_matmul_int8.restype = _int
 lib.gptq_matmul_int8_gated.argtypes = [ctypes.POINTER(_Tokens), _i64, _i64, ctypes.POINTER(_Layer),
                                        ctypes.POINTER(_Layer), _i64, _int, _p, _int, _i64, _p]
 lib.gptq_matmul_int8_gated.restype = _int
+lib.gptq_linear_int8_ws_bytes.argtypes = [_i64, _i64]
+lib.gptq_linear_int8_ws_bytes.restype = ctypes.c_size_t
+lib.gptq_linear_int8.argtypes = [_p, _int, _i64, _i64, _i64, ctypes.POINTER(_Layer), _i64, _p, _p, _int, _i64, _p,
+                                 ctypes.c_size_t, _p]
+lib.gptq_linear_int8.restype = _int
+lib.gptq_linear_int8_gated.argtypes = [_p, _int, _i64, _i64, _i64, ctypes.POINTER(_Layer), ctypes.POINTER(_Layer),
+                                       _i64, _int, _p, _int, _i64, _p, ctypes.c_size_t, _p]
+lib.gptq_linear_int8_gated.restype = _int
 lib.gptq_int8_status.argtypes = [_p]
 lib.gptq_int8_status.restype = _int
 
@@ -76,33 +84,47 @@ class Int8Tokens(NamedTuple):
 
 # ------------------------------------------------------------------ checks
 # The library sees addresses only: types, shapes and devices are checked here.
+# At decode these lines cost as much as the kernels they launch, so they touch
+# each tensor's attributes as few times as they can.
+_CODES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _code(dtype):
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
+
+
 def _vector(t, n, dtype, device, name):
-    if t.dtype is not dtype or t.shape != (n,) or (n > 1 and t.stride(0) != 1) or t.device != device:
+    """The address of a contiguous vector."""
+    if t.dtype is not dtype or t.shape != (n,) or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} elements on {device}")
+    return t.data_ptr()
 
 
-def _matrix(t, rows, cols, dtype, device, name):
-    if t.dtype is not dtype or t.shape != (rows, cols) or t.device != device:
-        raise ValueError(f"{name} must be a {dtype} matrix of {rows} x {cols} on {device}")
-    _rows(t, name)
+def _matrix(t, shape, dtype, device, name):
+    """The address and row stride of a matrix with contiguous rows."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} matrix of {shape[0]} x {shape[1]} on {device}")
+    return t.data_ptr(), _ld(t, name)
 
 
-def _rows(t, name):
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+def _ld(t, name):
+    """The row stride; a single row's is of no account, and is given as the
+    shortest any call accepts."""
+    if t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
-
-
-def _ld(t):
-    """The row stride; a single row's is of no account."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _ld8(t):
-    return t.stride(0) if t.shape[0] > 1 else _round16(t.shape[1])
+    ld, one = t.stride()
+    rows, cols = t.shape
+    if one != 1 and cols > 1:
+        raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
+    return ld if rows > 1 else _round16(cols)
 
 
 def _round16(n):
-    return (n + 15) // 16 * 16
+    return (n + 15) & ~15
 
 
 def _int8_rows(rows, cols, device):
@@ -114,159 +136,167 @@ def _c_tokens(x):
     q = x.q
     if q.dtype is not torch.int8:
         raise ValueError(f"x.q must be int8, got {q.dtype}")
-    _rows(q, "x.q")
-    _vector(x.scale, q.shape[0], torch.float32, q.device, "x.scale")
-    _vector(x.sum, q.shape[0], torch.int32, q.device, "x.sum")
-    return _Tokens(q.data_ptr(), _ld8(q), x.scale.data_ptr(), x.sum.data_ptr())
+    ld, n, dev = _ld(q, "x.q"), q.shape[0], q.device
+    return _Tokens(q.data_ptr(), ld, _vector(x.scale, n, torch.float32, dev, "x.scale"),
+                   _vector(x.sum, n, torch.int32, dev, "x.sum"))
 
 
 def _c_layer(layer, in_, device, name):
-    weight, scale, zero = layer if len(layer) == 3 else (*layer, None)
+    """(the C struct, the channels) of an Int8Layer or (weight, scale[, zero])."""
+    weight, scale = layer[0], layer[1]
+    zero = layer[2] if len(layer) > 2 else None
     if weight.dim() != 2:
         raise ValueError(f"{name}: the weight must be a 2-D tensor")
     out = weight.shape[0]
-    _matrix(weight, out, in_, torch.int8, device, f"{name}: the weight")
-    _vector(scale, out, torch.float32, device, f"{name}: the scale")
-    if zero is not None:
-        _vector(zero, out, torch.int32, device, f"{name}: the zero")
-    return _Layer(weight.data_ptr(), _ld8(weight), scale.data_ptr(), None if zero is None else zero.data_ptr()), out
+    w, ld = _matrix(weight, (out, in_), torch.int8, device, f"{name}.weight")
+    return _Layer(w, ld, _vector(scale, out, torch.float32, device, f"{name}.scale"),
+                  None if zero is None else _vector(zero, out, torch.int32, device, f"{name}.zero")), out
 
 
-class _on:
-    """The tensors' device as the current one for a call."""
-
-    def __init__(self, t):
-        if not t.is_cuda:
-            raise ValueError(f"the tensors must be on a CUDA device, not {t.device}")
-        index = t.device.index
-        self.guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(device, stream, fn, *args):
+    """fn on the tensors' device and the stream (None: its current one)."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors must be on a CUDA device, not {device}")
+    index = device.index
+    raw = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, raw)
+    if status:
+        _check(status)
 
 
 # --------------------------------------------------------------- ABI calls
 def gptq_layout_int8(qweight, zeros, bits, weight, zero=None, stream=None) -> None:
     """weight (int8, out x in) and zero (int32, out) of a layer solved with
     one group per row, from its packed codes and zeros (int32, out or out x 1)."""
-    _rows(weight, "weight")
-    out, in_ = weight.shape
     dev = weight.device
     if weight.dtype is not torch.int8:
         raise ValueError(f"weight must be int8, got {weight.dtype}")
+    ld = _ld(weight, "weight")
+    out, in_ = weight.shape
     if qweight.dtype not in (torch.int32, torch.uint32) or not qweight.is_contiguous() or \
             qweight.numel() != out * in_ * bits // 32 or qweight.device != dev:
         raise ValueError(f"qweight must hold {out} contiguous rows of {in_ * bits // 32} words on {dev}")
-    _vector(zeros.reshape(-1), out, torch.int32, dev, "zeros")
-    if zero is not None:
-        _vector(zero, out, torch.int32, dev, "zero")
-    with _on(weight):
-        _check(lib.gptq_layout_int8(_ptr(qweight), _ptr(zeros), out, in_, int(bits), _ptr(weight), _ld8(weight),
-                                    _ptr(zero), _stream(stream)))
+    z = _vector(zeros.reshape(-1), out, torch.int32, dev, "zeros")
+    z8 = None if zero is None else _vector(zero, out, torch.int32, dev, "zero")
+    _call(dev, stream, lib.gptq_layout_int8, qweight.data_ptr(), z, out, in_, int(bits), weight.data_ptr(), ld, z8)
 
 
 def gptq_quantize_tokens(X, q, scale, sum, stream=None) -> None:
     """q (int8), scale (float32) and sum (int32) <- X [tokens, in]."""
-    _rows(X, "X")
-    _matrix(q, *X.shape, torch.int8, X.device, "q")
-    _vector(scale, X.shape[0], torch.float32, X.device, "scale")
-    _vector(sum, X.shape[0], torch.int32, X.device, "sum")
-    with _on(X):
-        _check(lib.gptq_quantize_tokens(X.data_ptr(), _dt(X), *X.shape, _ld(X), q.data_ptr(), _ld8(q),
-                                        scale.data_ptr(), sum.data_ptr(), _stream(stream)))
+    ldx, code, dev = _ld(X, "X"), _code(X.dtype), X.device
+    T, in_ = X.shape
+    qp, ldq = _matrix(q, (T, in_), torch.int8, dev, "q")
+    _call(dev, stream, lib.gptq_quantize_tokens, X.data_ptr(), code, T, in_, ldx, qp, ldq,
+          _vector(scale, T, torch.float32, dev, "scale"), _vector(sum, T, torch.int32, dev, "sum"))
 
 
 def gptq_norm_tokens(h, y=None, weight=None, bias=None, post_weight=None, post_bias=None, gate=None, alpha=1.0,
-                     beta=1.0, kind="rms", eps=1e-6, h_out=None, x=None, tokens=None, dtype=None,
-                     stream=None) -> None:
+                     beta=1.0, kind="rms", eps=1e-6, h_out=None, x=None, tokens=None, stream=None) -> None:
     """h_out, x and/or tokens (an Int8Tokens) <- the norms around a block.
-    h_out may be h.  ``dtype`` names the type of weight and bias where neither
-    y nor x is given."""
-    _rows(h, "h")
-    T, d = h.shape
-    dev, ht = h.device, h.dtype
-    yt = next((t.dtype for t in (y, x, weight) if t is not None), dtype or ht)
+    h_out may be h."""
+    ldh, dev, ht = _ld(h, "h"), h.device, h.dtype
+    T, d = shape = h.shape
+    yt = y.dtype if y is not None else weight.dtype if weight is not None else ht
     if kind not in _NORMS:
         raise ValueError(f"kind must be one of {sorted(_NORMS)}, got {kind!r}")
-    for name, t, dt in (("y", y, yt), ("x", x, yt), ("h_out", h_out, ht)):
-        if t is not None:
-            _matrix(t, T, d, dt, dev, name)
-    for name, t in (("weight", weight), ("bias", bias), ("post_weight", post_weight), ("post_bias", post_bias)):
-        if t is not None:
-            _vector(t, d, yt, dev, name)
-    ldgate = 0
+
+    def matrix(t, dtype, name):
+        return (None, 0) if t is None else _matrix(t, shape, dtype, dev, name)
+
+    def vector(t, name):
+        return None if t is None else _vector(t, d, yt, dev, name)
+
     if gate is not None and gate.dim() == 2:
-        _matrix(gate, T, d, yt, dev, "gate")
-        ldgate = _ld(gate)
-    elif gate is not None:
-        _vector(gate, d, yt, dev, "gate")
-    a = _Norm(T, d, _dt(h), _dt_of(yt), _NORMS[kind], eps, alpha, beta, h.data_ptr(), _ld(h),
-              _at(y), 0 if y is None else _ld(y), _at(post_weight), _at(post_bias), _at(gate), ldgate,
-              _at(weight), _at(bias), _at(h_out), 0 if h_out is None else _ld(h_out),
-              _at(x), 0 if x is None else _ld(x), None, 0, None, None)
+        g, ldgate = _matrix(gate, shape, yt, dev, "gate")
+    else:
+        g, ldgate = vector(gate, "gate"), 0
+    a = _Norm(T, d, _code(ht), _code(yt), _NORMS[kind], eps, alpha, beta, h.data_ptr(), ldh, *matrix(y, yt, "y"),
+              vector(post_weight, "post_weight"), vector(post_bias, "post_bias"), g, ldgate,
+              vector(weight, "weight"), vector(bias, "bias"), *matrix(h_out, ht, "h_out"), *matrix(x, yt, "x"))
     if tokens is not None:
-        _matrix(tokens.q, T, d, torch.int8, dev, "tokens.q")
-        _vector(tokens.scale, T, torch.float32, dev, "tokens.scale")
-        _vector(tokens.sum, T, torch.int32, dev, "tokens.sum")
-        a.q, a.ldq, a.scale, a.sum = tokens.q.data_ptr(), _ld8(tokens.q), tokens.scale.data_ptr(), \
-            tokens.sum.data_ptr()
-    with _on(h):
-        _check(lib.gptq_norm_tokens(a, _stream(stream)))
+        a.q, a.ldq = _matrix(tokens.q, shape, torch.int8, dev, "tokens.q")
+        a.scale = _vector(tokens.scale, T, torch.float32, dev, "tokens.scale")
+        a.sum = _vector(tokens.sum, T, torch.int32, dev, "tokens.sum")
+    _call(dev, stream, lib.gptq_norm_tokens, a)
 
 
 def gptq_matmul_int8(x, layer, Y, bias=None, stream=None) -> None:
     """Y [tokens, out] <- the product of x (Int8Tokens) with an Int8Layer."""
-    xs = _c_tokens(x)
+    xs, dev = _c_tokens(x), x.q.device
     T, in_ = x.q.shape
-    w, out = _c_layer(layer, in_, x.q.device, "layer")
-    _matrix(Y, T, out, Y.dtype, x.q.device, "Y")
-    if bias is not None:
-        _vector(bias, out, torch.float32, x.q.device, "bias")
-    yt = _dt(Y)
-    with _on(x.q):
-        _check(lib.gptq_matmul_int8(xs, T, in_, w, out, _at(bias), Y.data_ptr(), yt, _ld(Y), _stream(stream)))
+    w, out = _c_layer(layer, in_, dev, "layer")
+    yt = _code(Y.dtype)
+    y, ldy = _matrix(Y, (T, out), Y.dtype, dev, "Y")
+    b = None if bias is None else _vector(bias, out, torch.float32, dev, "bias")
+    _call(dev, stream, lib.gptq_matmul_int8, xs, T, in_, w, out, b, y, yt, ldy)
 
 
 def gptq_matmul_int8_gated(x, gate, up, Y, act="silu", stream=None) -> None:
     """Y [tokens, out] <- act(x gate^T) * (x up^T)."""
-    xs = _c_tokens(x)
+    xs, dev = _c_tokens(x), x.q.device
     T, in_ = x.q.shape
-    dev = x.q.device
+    wg, wu, out, code = _c_pair(gate, up, in_, dev, act)
+    yt = _code(Y.dtype)
+    y, ldy = _matrix(Y, (T, out), Y.dtype, dev, "Y")
+    _call(dev, stream, lib.gptq_matmul_int8_gated, xs, T, in_, wg, wu, out, code, y, yt, ldy)
+
+
+def gptq_linear_int8_ws_bytes(tokens: int, in_: int) -> int:
+    return lib.gptq_linear_int8_ws_bytes(tokens, in_)
+
+
+def gptq_linear_int8(X, layer, Y, ws=None, bias=None, stream=None) -> None:
+    """Y [tokens, out] <- the product of floating activations X [tokens, in],
+    quantized by token, with an Int8Layer.  ws: a workspace tensor of
+    gptq_linear_int8_ws_bytes bytes (none where that is 0)."""
+    ldx, xt, dev = _ld(X, "X"), _code(X.dtype), X.device
+    T, in_ = X.shape
+    w, out = _c_layer(layer, in_, dev, "layer")
+    yt = _code(Y.dtype)
+    y, ldy = _matrix(Y, (T, out), Y.dtype, dev, "Y")
+    b = None if bias is None else _vector(bias, out, torch.float32, dev, "bias")
+    wsp, nws = _workspace(ws, dev)
+    _call(dev, stream, lib.gptq_linear_int8, X.data_ptr(), xt, T, in_, ldx, w, out, b, y, yt, ldy, wsp, nws)
+
+
+def gptq_linear_int8_gated(X, gate, up, Y, ws=None, act="silu", stream=None) -> None:
+    """Y [tokens, out] <- act(X gate^T) * (X up^T), X as in gptq_linear_int8."""
+    ldx, xt, dev = _ld(X, "X"), _code(X.dtype), X.device
+    T, in_ = X.shape
+    wg, wu, out, code = _c_pair(gate, up, in_, dev, act)
+    yt = _code(Y.dtype)
+    y, ldy = _matrix(Y, (T, out), Y.dtype, dev, "Y")
+    wsp, nws = _workspace(ws, dev)
+    _call(dev, stream, lib.gptq_linear_int8_gated, X.data_ptr(), xt, T, in_, ldx, wg, wu, out, code, y, yt, ldy, wsp,
+          nws)
+
+
+def _c_pair(gate, up, in_, dev, act):
     wg, out = _c_layer(gate, in_, dev, "gate")
     wu, out_up = _c_layer(up, in_, dev, "up")
     if out_up != out:
         raise ValueError(f"gate and up differ in size: {out} and {out_up} channels")
     if act not in _ACTS:
         raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
-    _matrix(Y, T, out, Y.dtype, dev, "Y")
-    yt = _dt(Y)
-    with _on(x.q):
-        _check(lib.gptq_matmul_int8_gated(xs, T, in_, wg, wu, out, _ACTS[act], Y.data_ptr(), yt, _ld(Y),
-                                          _stream(stream)))
+    return wg, wu, out, _ACTS[act]
+
+
+def _workspace(ws, dev):
+    if ws is None:
+        return None, 0
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {dev}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def gptq_int8_status(stream=None) -> None:
     """Wait for the stream and raise GptqError if a bounded device-side wait
     of an int8 product on this device has given up since the last call."""
     _check(lib.gptq_int8_status(_stream(stream)))
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
-_DTYPE_CODES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
-
-
-def _dt_of(dtype):
-    if dtype not in _DTYPE_CODES:
-        raise TypeError(f"unsupported dtype {dtype}")
-    return _DTYPE_CODES[dtype]
 
 
 # ---------------------------------------------------------- allocating calls
@@ -287,12 +317,15 @@ def int8_layer(r, bits: int) -> Int8Layer:
     return Int8Layer(weight, scales.reshape(-1), zero)
 
 
+def _new_tokens(T, d, dev):
+    return Int8Tokens(_int8_rows(T, d, dev), torch.empty(T, dtype=torch.float32, device=dev),
+                      torch.empty(T, dtype=torch.int32, device=dev))
+
+
 def quantize_tokens(X) -> Int8Tokens:
     """X [tokens, in] (f16, bf16 or f32) with a scale for each token."""
-    _rows(X, "X")
-    T, in_ = X.shape
-    x = Int8Tokens(_int8_rows(T, in_, X.device), torch.empty(T, dtype=torch.float32, device=X.device),
-                   torch.empty(T, dtype=torch.int32, device=X.device))
+    _ld(X, "X")
+    x = _new_tokens(*X.shape, X.device)
     gptq_quantize_tokens(X, *x)
     return x
 
@@ -308,41 +341,53 @@ def norm_tokens(h, y=None, weight=None, *, bias=None, post_weight=None, post_bia
     vector over channels or a [tokens, d] matrix.  kind is "rms" or "layer".
     ``quantize`` returns x as Int8Tokens; ``inplace`` writes h' over h.
     Without y and with alpha 1, h' is h and h itself is returned."""
-    _rows(h, "h")
     if weight is None:
         raise ValueError("weight (the pre-norm's) is needed")
+    _ld(h, "h")
     T, d = h.shape
-    h_out = h if inplace else None if y is None and alpha == 1.0 else torch.empty((T, d), dtype=h.dtype,
-                                                                                  device=h.device)
-    if quantize:
-        x, tokens = None, Int8Tokens(_int8_rows(T, d, h.device), torch.empty(T, dtype=torch.float32, device=h.device),
-                                     torch.empty(T, dtype=torch.int32, device=h.device))
-    else:
-        x, tokens = torch.empty((T, d), dtype=weight.dtype, device=h.device), None
+    dev = h.device
+    h_out = h if inplace else None if y is None and alpha == 1.0 else torch.empty((T, d), dtype=h.dtype, device=dev)
+    x, tokens = (None, _new_tokens(T, d, dev)) if quantize else \
+        (torch.empty((T, d), dtype=weight.dtype, device=dev), None)
     gptq_norm_tokens(h, y, weight, bias, post_weight, post_bias, gate, alpha, beta, kind, eps, h_out, x, tokens)
     return (h if h_out is None else h_out), (tokens if quantize else x)
+
+
+def _ws_for(x, device):
+    n = lib.gptq_linear_int8_ws_bytes(*x.shape)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 
 def linear_int8(x, layer, bias=None, dtype=None):
     """x [tokens, in] times an Int8Layer (or (weight, scale[, zero])), plus
     bias (float32).  A floating x is quantized by token first; the result has
     ``dtype``, by default x's (bfloat16 for Int8Tokens)."""
-    if not isinstance(x, Int8Tokens):
-        dtype = dtype or x.dtype
-        x = quantize_tokens(x)
-    Y = torch.empty((x.q.shape[0], layer[0].shape[0]), dtype=dtype or torch.bfloat16, device=x.q.device)
-    gptq_matmul_int8(x, layer, Y, bias)
+    out = layer[0].shape[0]
+    if isinstance(x, Int8Tokens):
+        q = x.q
+        Y = torch.empty((q.shape[0], out), dtype=dtype or torch.bfloat16, device=q.device)
+        gptq_matmul_int8(x, layer, Y, bias)
+    else:
+        _ld(x, "x")
+        dev = x.device
+        Y = torch.empty((x.shape[0], out), dtype=dtype or x.dtype, device=dev)
+        gptq_linear_int8(x, layer, Y, _ws_for(x, dev), bias)
     return Y
 
 
 def gated_int8(x, gate, up, act="silu", dtype=None):
     """act(x gate^T) * (x up^T) in one kernel; x, gate, up and dtype as in
     linear_int8, act one of "silu", "gelu", "gelu_tanh"."""
-    if not isinstance(x, Int8Tokens):
-        dtype = dtype or x.dtype
-        x = quantize_tokens(x)
-    Y = torch.empty((x.q.shape[0], gate[0].shape[0]), dtype=dtype or torch.bfloat16, device=x.q.device)
-    gptq_matmul_int8_gated(x, gate, up, Y, act)
+    out = gate[0].shape[0]
+    if isinstance(x, Int8Tokens):
+        q = x.q
+        Y = torch.empty((q.shape[0], out), dtype=dtype or torch.bfloat16, device=q.device)
+        gptq_matmul_int8_gated(x, gate, up, Y, act)
+    else:
+        _ld(x, "x")
+        dev = x.device
+        Y = torch.empty((x.shape[0], out), dtype=dtype or x.dtype, device=dev)
+        gptq_linear_int8_gated(x, gate, up, Y, _ws_for(x, dev), act)
     return Y
 
 

@@ -10,10 +10,10 @@ FLOOR = {torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -134, torch.float32: 
 
 
 def quantize(x):
-    """Codes and scales of float32 rows, with the definition's two float32
-    roundings (numpy's float32 division is IEEE)."""
+    """Codes and scales of float32 rows, with the definition's float32
+    roundings (numpy's float32 operations are IEEE)."""
     x = np.asarray(x, np.float32)
-    scale = (np.abs(x).max(1) / np.float32(127)).astype(np.float32)
+    scale = np.abs(x).max(1) * (np.float32(1) / np.float32(127))
     bad = ~np.isfinite(x).all(1)
     with np.errstate(all="ignore"):
         q = np.clip(np.rint(x / scale[:, None]), -127, 127)
