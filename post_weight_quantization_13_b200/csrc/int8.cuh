@@ -63,6 +63,27 @@ __device__ __forceinline__ void store8(T* __restrict__ p, const float* v, int le
   }
 }
 
+// ------------------------------------------------------------ tensor cores
+// Instruction descriptor of kind::i8: 32-bit integer accumulator (bits 4-5 =
+// 2), both operands signed (bits 7-9 and 10-12 = 1) and K-major, N >> 3 at
+// bits 17-22, M >> 4 at bits 24-28.
+__host__ __device__ constexpr uint32_t idesc_i8(uint32_t M, uint32_t N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
 // ------------------------------------------------------------ token quantizer
 // s = RN(max |x| RN(1/127)), code = clamp(rint(RN(x / s)), -127, 127), fp32.
 // top: the bit pattern of the row's largest magnitude, where NaN and infinity

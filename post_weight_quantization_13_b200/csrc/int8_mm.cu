@@ -71,25 +71,6 @@ __device__ __forceinline__ void umma_i8(uint32_t d, uint64_t a, uint64_t b, uint
       : "memory");
 }
 
-// Instruction descriptor of kind::i8: 32-bit integer accumulator (bits 4-5 =
-// 2), both operands signed (bits 7-9 and 10-12 = 1) and K-major, N >> 3 at
-// bits 17-22, M >> 4 at bits 24-28.
-__host__ __device__ constexpr uint32_t idesc_i8(uint32_t M, uint32_t N) {
-  return (2u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
-}
-
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
 __device__ __forceinline__ int4 ld_cluster_int4(uint32_t addr) {
   int4 v;
   asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
@@ -333,6 +314,8 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+}  // namespace
+
 // A K-major int8 operand (rows x in, row stride ld bytes) in boxes of
 // box_rows rows by 128 bytes; what lies past the matrix reads as zero.
 bool int8_map(CUtensorMap* m, const int8_t* base, int64_t rows, int64_t in, int64_t ld, int box_rows) {
@@ -346,6 +329,8 @@ bool int8_map(CUtensorMap* m, const int8_t* base, int64_t rows, int64_t in, int6
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 template <int G, typename T>
 cudaError_t launch_split(const SplitMaps& maps, const MmParams& kp, int64_t tiles, cudaStream_t st) {
@@ -427,9 +412,18 @@ cudaError_t run(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const g
 // Whether the rows kernel (int8_rows.cu) takes a product.
 bool few(int64_t tokens) { return tokens <= 4; }
 
+// Whether the pair kernel (int8_pair.cu) does.
+bool many(int64_t tokens) { return tokens > 512; }
+
 cudaError_t multiply(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const gptq_int8_layer_t* const (&w)[2],
                      int64_t out, const float* bias, int act, void* Y, gptq_dtype_t yt, int64_t ldy, cudaStream_t st) {
   if (few(tokens)) return rows_int8(nullptr, 0, 0, x, tokens, in, w, out, bias, act, Y, yt, ldy, st);
+  if (many(tokens)) {
+    void* status = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&status, g_int8_status);
+    if (e != cudaSuccess) return e;
+    return pair_int8(x, tokens, in, w, out, bias, act, Y, yt, ldy, (uint32_t*)status, st);
+  }
   if (w[1]) return run<2>(x, tokens, in, w, out, bias, act, Y, yt, ldy, st);
   return run<1>(x, tokens, in, w, out, bias, act, Y, yt, ldy, st);
 }

@@ -1,0 +1,379 @@
+// 8-bit integer products for many tokens, plain and gated.
+//
+// Bound by the tensor cores, and close behind by the operands' way from L2:
+// an SM multiplies 128 x 256 x 128 bytes in 512 cycles, and a CTA on its own
+// would have to load 48 KB for that.  So two CTAs on neighbouring SMs work as
+// one (cta_group::2): the pair owns 256 tokens x up to 256 channels, each CTA
+// loads its 128 tokens and half of the channels, and one tcgen05.mma reads
+// both halves from both shared memories: 32 KB per CTA and 512 cycles.  In
+// the gated form the first CTA's half are gate channels and the second's the
+// same up channels, so a thread finds both factors of an output in its own
+// tensor-memory lane.
+//
+// Persistent pairs, one per two SMs, warp-specialised in each CTA:
+//   warp 0     TMA producer: its own operand halves; the transactions of both
+//              CTAs are counted on the first CTA's barrier
+//   warp 1     (first CTA) issues the pair's MMAs and commits them to both
+//   warps 2-5  epilogue: scales, bias or activation, and 128-byte row pieces
+//              through shared memory to coalesced stores
+// Two 256-column accumulators in tensor memory let a tile's epilogue run
+// under the next tile's main loop.  Every wait is bounded (see split kernel).
+#include <algorithm>
+#include <cstring>
+
+#include "gemm.cuh"
+#include "int8.cuh"
+#include "internal.cuh"
+
+namespace gptq {
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kBK = 128;                     // bytes of k per stage
+constexpr int kATile = 128 * kBK;            // a CTA's tokens of one stage
+constexpr int kStageOut = 4 * 32 * 128;      // epilogue staging: 32 rows x 128 bytes a warp
+constexpr int kVectors = 256 * 3 * 4;        // a tile's scales, zeros, bias
+constexpr int kGroup = 8;                    // token tiles that walk the channels together
+
+struct PairParams {
+  const float* tscale;
+  const int32_t* tsum;
+  const float* wscale[2];
+  const int32_t* wzero[2];
+  const float* bias;
+  void* Y;
+  int64_t ldy;
+  int tokens, out, act, vec;
+  int ktiles, bn, stages, stage_bytes;
+  int mtiles, ntiles, tiles, pairs;
+  uint32_t* status;
+};
+
+struct PairMaps {
+  CUtensorMap x;
+  CUtensorMap w[2];
+};
+
+__device__ __forceinline__ void umma_i8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on both CTAs' barrier at this offset once this thread's MMAs are done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// A tile into this CTA's shared memory, counted on a barrier of the pair
+// given by its cluster address.
+__device__ __forceinline__ void load_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The tile's first token and first channel.  kGroup token tiles walk the
+// channel tiles side by side, so the pairs at work share both operands in L2.
+__device__ __forceinline__ void tile_at(const PairParams& kp, int tile, int* mt, int* nt) {
+  const int group = tile / (kGroup * kp.ntiles), rest = tile - group * kGroup * kp.ntiles;
+  const int rows = min(kGroup, kp.mtiles - group * kGroup);
+  *mt = group * kGroup + rest % rows;
+  *nt = rest / rows;
+}
+
+template <int G, typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    int8_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ PairParams kp) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* staging = smem + (size_t)kp.stages * kp.stage_bytes;
+  float* vectors = (float*)(staging + kStageOut);
+  uint64_t* full = (uint64_t*)((uint8_t*)vectors + kVectors);
+  uint64_t* empty = full + kp.stages;
+  uint64_t* acc_full = empty + kp.stages;  // [2]
+  uint64_t* acc_empty = acc_full + 2;      // [2], the first CTA's count
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = (uint32_t*)(drain + 1);
+  volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+  volatile int* epilogue_abort = abort_flag + 1;  // written and read between the epilogue warps' barriers only
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const int half = kp.bn / 2;  // channels a CTA loads
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kp.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 8);  // four epilogue warps of each CTA
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *epilogue_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  const int pair = (int)blockIdx.x / 2;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const int stages = kp.stages, stage_bytes = kp.stage_bytes, ktiles = kp.ktiles;
+      const uint32_t bytes = 2u * (uint32_t)(kATile + half * kBK);  // of both CTAs
+      const CUtensorMap* wmap = &maps.w[G == 2 ? rank : 0];
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int tile = pair; tile < kp.tiles && !*abort_flag; tile += kp.pairs) {
+        int mt, nt;
+        tile_at(kp, tile, &mt, &nt);
+        const int t0 = mt * 256 + rank * 128;
+        const int n0 = G == 2 ? nt * half : nt * kp.bn + rank * half;
+        for (int kt = 0; kt < ktiles; ++kt) {
+          if (!mbar_wait(&empty[stage], phase ^ 1)) {
+            raise_status(kp.status, ST_TIMEOUT);
+            *abort_flag = 1;
+          }
+          if (*abort_flag) break;
+          uint8_t* sb = smem + (size_t)stage * stage_bytes;
+          const uint32_t bar = map_to_rank(smem_u32(&full[stage]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], bytes);
+          load_pair(sb, &maps.x, bar, kt * kBK, t0);
+          load_pair(sb + kATile, wmap, bar, kt * kBK, n0);
+          if (++stage == stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      const int stages = kp.stages, stage_bytes = kp.stage_bytes, ktiles = kp.ktiles;
+      const uint32_t idesc = idesc_i8(256, (uint32_t)kp.bn);
+      int stage = 0, step = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = pair; tile < kp.tiles && ok && !*abort_flag; tile += kp.pairs, ++step) {
+        const int buf = step & 1, use = step >> 1;
+        if (use > 0 && !mbar_wait(&acc_empty[buf], (use - 1) & 1)) {
+          raise_status(kp.status, ST_TIMEOUT);
+          *abort_flag = 1;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tbase + (uint32_t)buf * 256u;
+        for (int kt = 0; kt < ktiles; ++kt) {
+          if (!mbar_wait(&full[stage], phase)) {
+            raise_status(kp.status, ST_TIMEOUT);
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sb = smem_u32(smem + (size_t)stage * stage_bytes);
+#pragma unroll
+          for (int kk = 0; kk < kBK / 32; ++kk)
+            umma_i8_pair(d, smem_desc_k_sw128(sb + kk * 32), smem_desc_k_sw128(sb + kATile + kk * 32), idesc,
+                         (kt > 0 || kk > 0) ? 1u : 0u);
+          commit_pair(&empty[stage]);
+          if (++stage == stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (ok) commit_pair(&acc_full[buf]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    constexpr int CW = 128 / (int)sizeof(T);  // columns of a 128-byte row piece
+    const int quarter = warp & 3, e = threadIdx.x - 64;
+    const int bn = kp.bn, width = G == 2 ? half : bn;  // channels of the tile's output
+    uint8_t* mine = staging + (warp - 2) * (32 * 128);
+    float* const vscale = vectors;                 // [bn]: gated, gate then up
+    int* const vzero = (int*)(vectors + 256);      // [bn]
+    float* const vbias = vectors + 512;            // [bn]
+    int step = 0;
+    for (int tile = pair; tile < kp.tiles; tile += kp.pairs, ++step) {
+      int mt, nt;
+      tile_at(kp, tile, &mt, &nt);
+      const int n0 = nt * width;
+      const int t = mt * 256 + rank * 128 + quarter * 32 + lane;
+      // the tile's vectors, while its main loop runs
+      named_bar_sync(1, 128);  // the previous tile's are no longer read
+      for (int i = e; i < bn; i += 128) {
+        const int g = G == 2 ? i / half : 0, n = n0 + (G == 2 ? i % half : i);
+        const bool in = n < kp.out;
+        vscale[i] = in ? __ldg(kp.wscale[g] + n) : 0.f;
+        vzero[i] = in && kp.wzero[g] ? __ldg(kp.wzero[g] + n) : 0;
+        vbias[i] = G == 1 && in && kp.bias ? __ldg(kp.bias + n) : 0.f;
+      }
+      const float ts = t < kp.tokens ? __ldg(kp.tscale + t) : 0.f;
+      const int sum = t < kp.tokens ? __ldg(kp.tsum + t) : 0;
+      named_bar_sync(1, 128);
+      const int buf = step & 1, use = step >> 1;
+      if (!mbar_wait_sleep(&acc_full[buf], use & 1)) {
+        raise_status(kp.status, ST_TIMEOUT);
+        *abort_flag = 1;
+      }
+      if (*abort_flag) *epilogue_abort = 1;
+      // all four warps leave together: they share barrier 1
+      named_bar_sync(1, 128);
+      if (*epilogue_abort) break;
+      tc_fence_after();
+      const uint32_t tmem = tbase + (uint32_t)buf * 256u + ((uint32_t)(quarter * 32) << 16);
+      T* const rows = (T*)kp.Y + (int64_t)(t - lane) * kp.ldy;
+      const int live = min(32, kp.tokens - (t - lane));  // rows of this warp inside the result
+      for (int c0 = 0; c0 < width; c0 += CW) {
+#pragma unroll
+        for (int p = 0; p < CW / 32; ++p) {
+          const int c = c0 + 32 * p;
+          float a[32], b[32];
+          tmem_ld32(tmem + (uint32_t)c, a);
+          if (G == 2) tmem_ld32(tmem + (uint32_t)(half + c), b);
+          alignas(16) T o[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float y = scaled(__float_as_int(a[i]), vzero[c + i], sum, ts, vscale[c + i]);
+            if (G == 2)
+              y = activate(y, kp.act) * scaled(__float_as_int(b[i]), vzero[half + c + i], sum, ts, vscale[half + c + i]);
+            else
+              y += vbias[c + i];
+            o[i] = from_f32<T>(y);
+          }
+          // 16-byte unit u of row r sits at unit u ^ (r & 7): neither the row
+          // owner's writes nor the row-wise reads below meet in a bank
+#pragma unroll
+          for (int u = 0; u < 2 * (int)sizeof(T); ++u)
+            *reinterpret_cast<uint4*>(mine + sw128(lane, p * 2 * (int)sizeof(T) + u)) =
+                reinterpret_cast<const uint4*>(o)[u];
+        }
+        if (c0 + CW >= width) {
+          // the accumulator is read: the next tile but one may have it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_remote(map_to_rank(smem_u32(&acc_empty[buf]), 0));
+        }
+        __syncwarp();
+        if (kp.vec && n0 + c0 + CW <= kp.out) {
+#pragma unroll
+          for (int r0 = 0; r0 < 32; r0 += 4) {
+            const int r = r0 + (lane >> 3);
+            if (r < live)
+              *reinterpret_cast<uint4*>((uint8_t*)(rows + r * kp.ldy + n0 + c0) + 16 * (lane & 7)) =
+                  *reinterpret_cast<const uint4*>(mine + sw128(r, lane & 7));
+          }
+        } else {
+          const int cols = min(CW, kp.out - n0 - c0);
+          for (int r = 0; r < live; ++r)
+            for (int c = lane; c < cols; c += 32) {
+              const int byte = c * (int)sizeof(T);
+              rows[r * kp.ldy + n0 + c0 + c] = *reinterpret_cast<const T*>(mine + sw128(r, byte >> 4) + (byte & 15));
+            }
+        }
+        __syncwarp();
+      }
+    }
+  }
+
+  __syncwarp();
+  if (*abort_flag && threadIdx.x == 32 && rank == 0) {
+    // let the MMAs already issued finish before the memory goes away
+    commit_pair(drain);
+    mbar_wait(drain, 0);
+  }
+  if (*abort_flag && threadIdx.x == 0) {  // and the copies
+    const uint64_t start = globaltimer();
+    while (globaltimer() - start < 1000000ull) {
+    }
+  }
+  __syncwarp();
+  // neither CTA leaves while the other's MMAs, commits or arrivals reach it
+  cluster_arrive();
+  cluster_wait();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(512u) : "memory");
+  }
+}
+
+template <int G, typename T>
+cudaError_t launch(const PairMaps& maps, const PairParams& kp, cudaStream_t st) {
+  const void* f = (const void*)int8_pair_kernel<G, T>;
+  cudaError_t e = ensure_smem_limit(f, 232448);
+  if (e != cudaSuccess) return e;
+  const size_t smem = 1024 + (size_t)kp.stages * kp.stage_bytes + kStageOut + kVectors + 256;
+  int8_pair_kernel<G, T><<<2 * kp.pairs, kThreads, smem, st>>>(maps, kp);
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t pair_int8(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const gptq_int8_layer_t* const (&w)[2],
+                      int64_t out, const float* bias, int act, void* Y, gptq_dtype_t yt, int64_t ldy, uint32_t* status,
+                      cudaStream_t st) {
+  const int G = w[1] ? 2 : 1;
+  PairParams kp = {};
+  kp.tscale = x->scale;
+  kp.tsum = x->sum;
+  for (int g = 0; g < G; ++g) {
+    kp.wscale[g] = w[g]->scale;
+    kp.wzero[g] = w[g]->zero;
+  }
+  kp.bias = bias;
+  kp.Y = Y;
+  kp.ldy = ldy;
+  kp.tokens = (int)tokens;
+  kp.out = (int)out;
+  kp.act = act;
+  kp.vec = (uintptr_t)Y % 16 == 0 && (ldy * (yt == GPTQ_F32 ? 4 : 2)) % 16 == 0;
+  kp.status = status;
+  kp.ktiles = (int)((in + kBK - 1) / kBK);
+  kp.bn = 256;
+  kp.stage_bytes = kATile + kp.bn / 2 * kBK;
+  kp.stages = std::min(12, (232448 - 1024 - kStageOut - kVectors - 256) / kp.stage_bytes);
+  kp.mtiles = (int)((tokens + 255) / 256);
+  const int width = kp.bn / G;
+  kp.ntiles = (int)((out + width - 1) / width);
+  kp.tiles = kp.mtiles * kp.ntiles;
+  kp.pairs = std::min(kp.tiles, device_info().sms / 2);
+  PairMaps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  if (!int8_map(&maps.x, x->q, tokens, in, x->ldq, 128)) return cudaErrorInvalidValue;
+  for (int g = 0; g < G; ++g)
+    if (!int8_map(&maps.w[g], w[g]->w, out, in, w[g]->ldw, kp.bn / 2)) return cudaErrorInvalidValue;
+  if (G == 2)
+    return yt == GPTQ_F16    ? launch<2, __half>(maps, kp, st)
+           : yt == GPTQ_BF16 ? launch<2, __nv_bfloat16>(maps, kp, st)
+                             : launch<2, float>(maps, kp, st);
+  return yt == GPTQ_F16    ? launch<1, __half>(maps, kp, st)
+         : yt == GPTQ_BF16 ? launch<1, __nv_bfloat16>(maps, kp, st)
+                           : launch<1, float>(maps, kp, st);
+}
+
+}  // namespace gptq

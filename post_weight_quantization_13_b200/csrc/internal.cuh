@@ -95,6 +95,14 @@ gptq_status_t linear_int8(const void* X, gptq_dtype_t xt, int64_t tokens, int64_
 cudaError_t rows_int8(const void* x, int xt, int64_t ldx, const gptq_int8_tokens_t* tokens8, int64_t tokens, int64_t in,
                       const gptq_int8_layer_t* const (&w)[2], int64_t out, const float* bias, int act, void* Y,
                       gptq_dtype_t yt, int64_t ldy, cudaStream_t st);
+// Both for many tokens (int8_pair.cu); a wait that gives up raises ST_TIMEOUT
+// in *status.
+cudaError_t pair_int8(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const gptq_int8_layer_t* const (&w)[2],
+                      int64_t out, const float* bias, int act, void* Y, gptq_dtype_t yt, int64_t ldy, uint32_t* status,
+                      cudaStream_t st);
+// A tensor map over a K-major int8 operand (rows x in, row stride ld bytes) in
+// boxes of box_rows rows by 128 bytes; what lies past the matrix reads as zero.
+bool int8_map(CUtensorMap* m, const int8_t* base, int64_t rows, int64_t in, int64_t ld, int box_rows);
 gptq_status_t int8_status(cudaStream_t st);
 // Checks of a workspace argument (abi.cu).
 gptq_status_t check_ws(void* ws, size_t ws_bytes, size_t need);
