@@ -92,6 +92,20 @@ __device__ __forceinline__ void tile_at(const PairParams& kp, int tile, int* mt,
   *nt = rest / rows;
 }
 
+// Sixteen columns of sums (32-bit integers in v) to the product's values.
+__device__ __forceinline__ void scale_columns(const float (&v)[16], float (&y)[16], const float* scale,
+                                              const int* zero, int sum, float ts) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    const float4 s = *reinterpret_cast<const float4*>(scale + i);
+    const int4 z = *reinterpret_cast<const int4*>(zero + i);
+    y[i + 0] = scaled(__float_as_int(v[i + 0]), z.x, sum, ts, s.x);
+    y[i + 1] = scaled(__float_as_int(v[i + 1]), z.y, sum, ts, s.y);
+    y[i + 2] = scaled(__float_as_int(v[i + 2]), z.z, sum, ts, s.z);
+    y[i + 3] = scaled(__float_as_int(v[i + 3]), z.w, sum, ts, s.w);
+  }
+}
+
 template <int G, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int8_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ PairParams kp) {
@@ -249,28 +263,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       T* const rows = (T*)kp.Y + (int64_t)(t - lane) * kp.ldy;
       const int live = min(32, kp.tokens - (t - lane));  // rows of this warp inside the result
       for (int c0 = 0; c0 < width; c0 += CW) {
+        // sixteen columns a step, not unrolled further: the loop has to stay
+        // in the instruction cache (unrolled over 64 columns, the gated form
+        // waited for instructions most of the time and took 1.6 times as long)
+#pragma unroll 1
+        for (int p = 0; p < CW / 16; ++p) {
+          const int c = c0 + 16 * p;
+          float a[16], y[16];
+          tmem_ld16(tmem + (uint32_t)c, a);
+          scale_columns(a, y, vscale + c, vzero + c, sum, ts);
+          if (G == 2) {
+            if (kp.act == GPTQ_ACT_GELU) {
 #pragma unroll
-        for (int p = 0; p < CW / 32; ++p) {
-          const int c = c0 + 32 * p;
-          float a[32], b[32];
-          tmem_ld32(tmem + (uint32_t)c, a);
-          if (G == 2) tmem_ld32(tmem + (uint32_t)(half + c), b);
-          alignas(16) T o[32];
+              for (int i = 0; i < 16; ++i) y[i] = activate(y[i], GPTQ_ACT_GELU);
+            } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float y = scaled(__float_as_int(a[i]), vzero[c + i], sum, ts, vscale[c + i]);
-            if (G == 2)
-              y = activate(y, kp.act) * scaled(__float_as_int(b[i]), vzero[half + c + i], sum, ts, vscale[half + c + i]);
-            else
-              y += vbias[c + i];
-            o[i] = from_f32<T>(y);
+              for (int i = 0; i < 16; ++i) y[i] = activate(y[i], kp.act);
+            }
+            float u[16];
+            tmem_ld16(tmem + (uint32_t)(half + c), a);
+            scale_columns(a, u, vscale + half + c, vzero + half + c, sum, ts);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] *= u[i];
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] += vbias[c + i];
           }
+          alignas(16) T o[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = from_f32<T>(y[i]);
           // 16-byte unit u of row r sits at unit u ^ (r & 7): neither the row
           // owner's writes nor the row-wise reads below meet in a bank
 #pragma unroll
-          for (int u = 0; u < 2 * (int)sizeof(T); ++u)
-            *reinterpret_cast<uint4*>(mine + sw128(lane, p * 2 * (int)sizeof(T) + u)) =
-                reinterpret_cast<const uint4*>(o)[u];
+          for (int u = 0; u < (int)sizeof(T); ++u)
+            *reinterpret_cast<uint4*>(mine + sw128(lane, p * (int)sizeof(T) + u)) = reinterpret_cast<const uint4*>(o)[u];
         }
         if (c0 + CW >= width) {
           // the accumulator is read: the next tile but one may have it
