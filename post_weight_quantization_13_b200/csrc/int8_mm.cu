@@ -10,12 +10,13 @@
 // split kernel: the weights' channels are the tensor core's 128 rows (tensor-
 // memory lanes), the tokens its columns (16 to 128), so a handful of tokens
 // still streams the weights through full-height MMAs.  The CTAs of a cluster
-// split k; their partial sums meet through distributed shared memory, where
-// each CTA adds and writes its share of the tokens.  Integer addition makes
+// split k; each pushes its partial sums through distributed shared memory to
+// the CTA that adds and writes that share of the tokens.  Integer addition makes
 // the result independent of the split, and no workspace or atomic is needed.
 //   warp 0     TMA producer (one thread)
 //   warp 1     tensor memory, tcgen05.mma.kind::i8 (one thread)
-//   warps 2-5  tensor memory -> shared memory, cluster reduction, epilogue
+//   warps 2-5  epilogue, or their partial sums into the shared memory of the
+//              rank that finishes the token, then that rank's epilogue
 // Every wait is bounded; a wait that gives up raises ST_TIMEOUT in the
 // library's int8 status word, and the CTA drains and leaves.
 #include <cuda_bf16.h>
@@ -37,6 +38,8 @@ constexpr int kBK = 128;                 // int8 elements of k per stage row (12
 constexpr int kTileM = 128;              // channels of a tile
 constexpr int kTileBytes = kTileM * kBK;
 constexpr int kMaxSplit = 8;             // portable cluster size
+constexpr int kMaxNTile = 256;           // tokens of a tile
+constexpr int kSmem = 232448, kSmemFixed = 1024 + 2 * 4 * kMaxNTile + 256;
 
 // Raised by bounded waits that gave up, read and cleared by gptq_int8_status.
 __device__ uint32_t g_int8_status;
@@ -52,7 +55,7 @@ struct MmParams {
   int tokens, out, in;
   int act;
   int vec;  // rows of Y start on 16-byte boundaries
-  int ktiles, split, ntile, stages, stage_bytes, tmem_cols, ctiles;
+  int ktiles, split, ntile, stages, stage_bytes, push_bytes, tmem_cols, ctiles;
 };
 
 struct SplitMaps {
@@ -71,13 +74,8 @@ __device__ __forceinline__ void umma_i8(uint32_t d, uint64_t a, uint64_t b, uint
       : "memory");
 }
 
-__device__ __forceinline__ int4 ld_cluster_int4(uint32_t addr) {
-  int4 v;
-  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster(uint32_t addr, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // ------------------------------------------------------------ split kernel
@@ -86,7 +84,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     int8_split_kernel(const __grid_constant__ SplitMaps maps, const __grid_constant__ MmParams kp) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint64_t* full = (uint64_t*)(smem + (size_t)kp.stages * kp.stage_bytes);
+  // partial sums pushed by the cluster, [source rank][g][token of this rank's share][channel]
+  int* pushed = (int*)(smem + (size_t)kp.stages * kp.stage_bytes);
+  float* tscale = (float*)((uint8_t*)pushed + kp.push_bytes);  // [ntile]
+  int* tsum = (int*)(tscale + kMaxNTile);
+  uint64_t* full = (uint64_t*)(tsum + kMaxNTile);
   uint64_t* empty = full + kp.stages;
   uint64_t* acc_full = empty + kp.stages;
   uint64_t* drain = acc_full + 1;
@@ -121,15 +123,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
+  // first phase of the cluster's barrier: every CTA has begun, its shared
+  // memory can be written to
+  if (split > 1) cluster_arrive();
 
   if (warp == 0) {
     if (lane == 0) {
       const int stages = kp.stages, stage_bytes = kp.stage_bytes;
       const uint32_t bytes = (uint32_t)(G * kTileBytes + ntile * kBK);
+      // The weights do not come from the kernel before this one: the first
+      // stages' are on their way before it has finished with the tokens.
+      const int ahead = min(stages, kt1 - kt0);
+      for (int i = 0; i < ahead; ++i) {
+        uint8_t* sb = smem + (size_t)i * stage_bytes;
+        mbar_arrive_expect_tx(&full[i], bytes);
+#pragma unroll
+        for (int g = 0; g < G; ++g) tma_load_2d(sb + g * kTileBytes, &maps.w[g], &full[i], (kt0 + i) * kBK, n0);
+      }
+      grid_dependency_wait();
+      for (int i = 0; i < ahead; ++i)
+        tma_load_2d(smem + (size_t)i * stage_bytes + G * kTileBytes, &maps.x, &full[i], (kt0 + i) * kBK, t0);
       int stage = 0;
       uint32_t phase = 0;
-      for (int kt = kt0; kt < kt1; ++kt) {
-        if (!mbar_wait(&empty[stage], phase ^ 1)) {
+      for (int kt = kt0 + ahead; kt < kt1; ++kt) {
+        if (!mbar_wait(&empty[stage], phase)) {
           raise_status(&g_int8_status, ST_TIMEOUT);
           *abort_flag = 1;
         }
@@ -145,6 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    __syncwarp();
+    if (split > 1) cluster_wait();
   } else if (warp == 1) {
     if (lane == 0) {
       const int stages = kp.stages, stage_bytes = kp.stage_bytes;
@@ -176,46 +195,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ok) umma_commit(acc_full);
     }
+    __syncwarp();
+    if (split > 1) cluster_wait();
   } else {
-    // partial sums -> shared memory, [g][token][channel]; the pipeline's
-    // stages are free once the accumulators are complete
-    const int quarter = warp & 3;
-    if (!mbar_wait_sleep(acc_full, 0)) {
-      raise_status(&g_int8_status, ST_TIMEOUT);
-      *abort_flag = 1;
-    } else {
-      tc_fence_after();
-      int* part = (int*)smem;
-      const int c = quarter * 32 + lane;
-      for (int j0 = 0; j0 < G * ntile; j0 += 16) {
-        float v[16];
-        tmem_ld16(tbase + (uint32_t)j0 + ((uint32_t)(quarter * 32) << 16), v);
+    const int quarter = warp & 3, e = threadIdx.x - 64;
+    const int c = quarter * 32 + lane;
+    const uint32_t tmem = tbase + ((uint32_t)(quarter * 32) << 16);
+    // Everything the epilogue reads from memory is fetched under the main
+    // loop.  A thread's channels: its lane of tensor memory, or four of a
+    // row where the sums come from shared memory.
+    constexpr int V = 4;
+    const int n = n0 + (split > 1 ? V * lane : c);
+    float ws[G][V], bias[V];
+    int wz[G][V];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) part[(j0 + j) * kTileM + c] = __float_as_int(v[j]);
-      }
-    }
-    tc_fence_before();
-  }
-  __syncwarp();
-  // every CTA's partial sums are in place (a CTA whose wait gave up arrives too)
-  if (split > 1) {
-    cluster_arrive();
-    cluster_wait();
-  } else {
-    __syncthreads();
-  }
-  if (warp >= 2) {
-    // rank r finishes tokens [ntile r / split, ntile (r + 1) / split): one
-    // token a warp, four channels a lane
-    const int j0 = ntile * rank / split, j1 = ntile * (rank + 1) / split;
-    const int n = n0 + 4 * lane;
-    const uint32_t part = smem_u32(smem);
-    float ws[G][4];
-    int wz[G][4];
-    float bias[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool in = n + i < kp.out;
+    for (int i = 0; i < V; ++i) {
+      const bool in = n + i < kp.out && (split > 1 || i == 0);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         ws[g][i] = in ? __ldg(kp.wscale[g] + n + i) : 0.f;
@@ -223,60 +218,113 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       bias[i] = G == 1 && in && kp.bias ? __ldg(kp.bias + n + i) : 0.f;
     }
-    for (int j = j0 + warp - 2; j < j1; j += 4) {
-      const int t = t0 + j;
-      if (t >= kp.tokens) break;
-      const float ts = __ldg(kp.tscale + t);
-      const int sum = __ldg(kp.tsum + t);
-      int acc[G][4];
+    grid_dependency_wait();
+    for (int j = e; j < ntile; j += 128) {
+      const bool in = t0 + j < kp.tokens;
+      tscale[j] = in ? kp.tscale[t0 + j] : 0.f;
+      tsum[j] = in ? kp.tsum[t0 + j] : 0;
+    }
+    named_bar_sync(1, 128);
+    const int live = min(ntile, kp.tokens - t0);  // tokens of the tile inside the result
+    bool ok = mbar_wait_sleep(acc_full, 0);
+    if (!ok) {
+      raise_status(&g_int8_status, ST_TIMEOUT);
+      *abort_flag = 1;
+    }
+    __syncwarp();
+    tc_fence_after();
+    if (split == 1) {
+      // a token at a time, 32 neighbouring channels a warp
+      T* const col = (T*)kp.Y + (int64_t)t0 * kp.ldy + n;
+#pragma unroll 1
+      for (int j0 = 0; j0 < live; j0 += 16) {
+        float a[16], u[16];
+        tmem_ld16(tmem + (uint32_t)j0, a);
+        if (G == 2) tmem_ld16(tmem + (uint32_t)(ntile + j0), u);
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const uint32_t at = part + (uint32_t)(((g * ntile + j) * kTileM + 4 * lane) * 4);
-        int4 a = make_int4(0, 0, 0, 0);
-        for (int r = 0; r < split; ++r) {
-          const int4 b = split > 1 ? ld_cluster_int4(map_to_rank(at, (uint32_t)r))
-                                   : *reinterpret_cast<const int4*>(smem + (at - part));
-          a.x += b.x;
-          a.y += b.y;
-          a.z += b.z;
-          a.w += b.w;
+        for (int i = 0; i < 16; ++i) {
+          const int j = j0 + i;
+          float y = scaled(__float_as_int(a[i]), wz[0][0], tsum[j], tscale[j], ws[0][0]);
+          if (G == 2)
+            y = activate(y, kp.act) * scaled(__float_as_int(u[i]), wz[G - 1][0], tsum[j], tscale[j], ws[G - 1][0]);
+          else
+            y += bias[0];
+          if (j < live && n < kp.out) col[(int64_t)j * kp.ldy] = from_f32<T>(y);
         }
-        acc[g][0] = a.x;
-        acc[g][1] = a.y;
-        acc[g][2] = a.z;
-        acc[g][3] = a.w;
       }
-      alignas(16) T o[4];
+      tc_fence_before();
+    } else {
+      // each token's sums go to the rank that finishes it
+      cluster_wait();
+      const int share = ntile / split;
+#pragma unroll 1
+      for (int j0 = 0; j0 < ntile; j0 += 16) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float y = scaled(acc[0][i], wz[0][i], sum, ts, ws[0][i]);
-        if (G == 2)
-          y = activate(y, kp.act) * scaled(acc[G - 1][i], wz[G - 1][i], sum, ts, ws[G - 1][i]);
-        else
-          y += bias[i];
-        o[i] = from_f32<T>(y);
+        for (int g = 0; g < G; ++g) {
+          float v[16];
+          tmem_ld16(tmem + (uint32_t)(g * ntile + j0), v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int owner = (j0 + i) / share, j = (j0 + i) % share;
+            st_cluster(map_to_rank(smem_u32(pushed + ((rank * G + g) * share + j) * kTileM + c), (uint32_t)owner),
+                       __float_as_int(v[i]));
+          }
+        }
       }
-      T* dst = (T*)kp.Y + (int64_t)t * kp.ldy + n;
-      if (kp.vec && n + 4 <= kp.out) {
-        if (sizeof(T) == 2)
-          *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(o);
-        else
-          *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(o);
-      } else {
+      tc_fence_before();
+      __syncwarp();
+      cluster_arrive();  // second phase: all partial sums are in place
+      cluster_wait();
+#pragma unroll 1
+      for (int j = warp - 2; j < share; j += 4) {
+        const int at = rank * share + j;
+        if (at >= live) break;
+        int acc[G][V];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n + i < kp.out) dst[i] = o[i];
+        for (int g = 0; g < G; ++g) {
+          int4 sum = make_int4(0, 0, 0, 0);
+          for (int r = 0; r < split; ++r) {
+            const int4 b = *reinterpret_cast<const int4*>(pushed + ((r * G + g) * share + j) * kTileM + V * lane);
+            sum.x += b.x;
+            sum.y += b.y;
+            sum.z += b.z;
+            sum.w += b.w;
+          }
+          acc[g][0] = sum.x;
+          acc[g][1] = sum.y;
+          acc[g][2] = sum.z;
+          acc[g][3] = sum.w;
+        }
+        alignas(16) T o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          float y = scaled(acc[0][i], wz[0][i], tsum[at], tscale[at], ws[0][i]);
+          if (G == 2)
+            y = activate(y, kp.act) * scaled(acc[G - 1][i], wz[G - 1][i], tsum[at], tscale[at], ws[G - 1][i]);
+          else
+            y += bias[i];
+          o[i] = from_f32<T>(y);
+        }
+        T* dst = (T*)kp.Y + (int64_t)(t0 + at) * kp.ldy + n;
+        if (kp.vec && n + V <= kp.out) {
+          if (sizeof(T) == 2)
+            *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(o);
+          else
+            *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (n + i < kp.out) dst[i] = o[i];
+        }
       }
     }
   }
-  __syncwarp();
-  // no CTA leaves while a peer still reads its partial sums
-  if (split > 1) {
+  if (split > 1 && warp < 2) {
     cluster_arrive();
     cluster_wait();
-  } else {
-    __syncthreads();
   }
+  grid_dependency_wait();
+  __syncthreads();
   if (*abort_flag) {
     // let copies and MMAs already issued finish before the memory goes away
     if (threadIdx.x == 32) {
@@ -333,22 +381,26 @@ bool int8_map(CUtensorMap* m, const int8_t* base, int64_t rows, int64_t in, int6
 namespace {
 
 template <int G, typename T>
-cudaError_t launch_split(const SplitMaps& maps, const MmParams& kp, int64_t tiles, cudaStream_t st) {
+cudaError_t launch_split(const SplitMaps& maps, const MmParams& kp, int64_t tiles, bool follows, cudaStream_t st) {
   const void* f = (const void*)int8_split_kernel<G, T>;
   cudaError_t e = ensure_smem_limit(f, 232448);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * kp.split));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = 1024 + (size_t)kp.stages * kp.stage_bytes + 256;
+  cfg.dynamicSmemBytes = (size_t)kSmemFixed + (size_t)kp.stages * kp.stage_bytes + kp.push_bytes;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)kp.split;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
   cfg.numAttrs = kp.split > 1 ? 1 : 0;
+  cfg.attrs = attr;
+  if (follows) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
   e = cudaLaunchKernelEx(&cfg, int8_split_kernel<G, T>, maps, kp);
   note_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -358,21 +410,21 @@ cudaError_t launch_split(const SplitMaps& maps, const MmParams& kp, int64_t tile
 // while the tiles leave SMs idle and every CTA keeps at least two k-tiles.
 template <int G>
 cudaError_t run_split(MmParams kp, const gptq_int8_tokens_t* x, const gptq_int8_layer_t* const (&w)[2],
-                      gptq_dtype_t yt, cudaStream_t st, int sms) {
-  kp.ntile = std::min(128, (kp.tokens + 15) / 16 * 16);
+                      gptq_dtype_t yt, bool follows, cudaStream_t st, int sms) {
+  kp.ntile = std::min(G == 2 ? 64 : 128, (kp.tokens + 15) / 16 * 16);
   kp.ctiles = (kp.out + kTileM - 1) / kTileM;
   kp.ktiles = (kp.in + kBK - 1) / kBK;
   const int64_t tiles = (int64_t)kp.ctiles * ((kp.tokens + kp.ntile - 1) / kp.ntile);
   kp.split = 1;
   while (kp.split < kMaxSplit && tiles * kp.split * 2 <= sms && kp.ktiles >= kp.split * 4) kp.split *= 2;
   kp.stage_bytes = G * kTileBytes + kp.ntile * kBK;
+  kp.push_bytes = kp.split > 1 ? G * kp.ntile * kTileM * 4 : 0;
   kp.tmem_cols = 32;
   while (kp.tmem_cols < G * kp.ntile) kp.tmem_cols *= 2;
   // The stages fill shared memory, so no two CTAs of these kernels share an
   // SM: a CTA that waits for tensor memory held by another could otherwise
   // hold up that one's cluster.
-  kp.stages = (232448 - 1024 - 256) / kp.stage_bytes;
-  if (kp.stages > 12) kp.stages = 12;
+  kp.stages = std::min(12, (kSmem - kSmemFixed - kp.push_bytes) / kp.stage_bytes);
   SplitMaps maps;
   std::memset(&maps, 0, sizeof(maps));
   for (int g = 0; g < G; ++g)
@@ -380,17 +432,18 @@ cudaError_t run_split(MmParams kp, const gptq_int8_tokens_t* x, const gptq_int8_
   if (!int8_map(&maps.x, x->q, kp.tokens, kp.in, x->ldq, kp.ntile)) return cudaErrorInvalidValue;
   switch (yt) {
     case GPTQ_F16:
-      return launch_split<G, __half>(maps, kp, tiles, st);
+      return launch_split<G, __half>(maps, kp, tiles, follows, st);
     case GPTQ_BF16:
-      return launch_split<G, __nv_bfloat16>(maps, kp, tiles, st);
+      return launch_split<G, __nv_bfloat16>(maps, kp, tiles, follows, st);
     default:
-      return launch_split<G, float>(maps, kp, tiles, st);
+      return launch_split<G, float>(maps, kp, tiles, follows, st);
   }
 }
 
 template <int G>
 cudaError_t run(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const gptq_int8_layer_t* const (&w)[2],
-                int64_t out, const float* bias, int act, void* Y, gptq_dtype_t yt, int64_t ldy, cudaStream_t st) {
+                int64_t out, const float* bias, int act, void* Y, gptq_dtype_t yt, int64_t ldy, bool follows,
+                cudaStream_t st) {
   MmParams kp = {};
   kp.tscale = x->scale;
   kp.tsum = x->sum;
@@ -406,26 +459,29 @@ cudaError_t run(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const g
   kp.in = (int)in;
   kp.act = act;
   kp.vec = (uintptr_t)Y % 16 == 0 && (ldy * (yt == GPTQ_F32 ? 4 : 2)) % 16 == 0;
-  return run_split<G>(kp, x, w, yt, st, device_info().sms);
+  return run_split<G>(kp, x, w, yt, follows, st, device_info().sms);
 }
 
 // Whether the rows kernel (int8_rows.cu) takes a product.
-bool few(int64_t tokens) { return tokens <= 4; }
+bool few(int64_t tokens) { return tokens <= 2; }
 
 // Whether the pair kernel (int8_pair.cu) does.
 bool many(int64_t tokens) { return tokens > 512; }
 
+// follows: the kernel launched before on st is the quantizer that wrote x, and
+// this one may be set up while it runs.
 cudaError_t multiply(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const gptq_int8_layer_t* const (&w)[2],
-                     int64_t out, const float* bias, int act, void* Y, gptq_dtype_t yt, int64_t ldy, cudaStream_t st) {
+                     int64_t out, const float* bias, int act, void* Y, gptq_dtype_t yt, int64_t ldy, bool follows,
+                     cudaStream_t st) {
   if (few(tokens)) return rows_int8(nullptr, 0, 0, x, tokens, in, w, out, bias, act, Y, yt, ldy, st);
   if (many(tokens)) {
     void* status = nullptr;
     const cudaError_t e = cudaGetSymbolAddress(&status, g_int8_status);
     if (e != cudaSuccess) return e;
-    return pair_int8(x, tokens, in, w, out, bias, act, Y, yt, ldy, (uint32_t*)status, st);
+    return pair_int8(x, tokens, in, w, out, bias, act, Y, yt, ldy, follows, (uint32_t*)status, st);
   }
-  if (w[1]) return run<2>(x, tokens, in, w, out, bias, act, Y, yt, ldy, st);
-  return run<1>(x, tokens, in, w, out, bias, act, Y, yt, ldy, st);
+  if (w[1]) return run<2>(x, tokens, in, w, out, bias, act, Y, yt, ldy, follows, st);
+  return run<1>(x, tokens, in, w, out, bias, act, Y, yt, ldy, follows, st);
 }
 
 // The workspace of a product that quantizes its tokens: codes, scales, sums.
@@ -444,7 +500,7 @@ struct TokenScratch {
 gptq_status_t matmul_int8(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const gptq_int8_layer_t* w,
                           int64_t out, const float* bias, void* Y, gptq_dtype_t yt, int64_t ldy, cudaStream_t st) {
   const gptq_int8_layer_t* const ws[2] = {w, nullptr};
-  CUDA_TRY(multiply(x, tokens, in, ws, out, bias, 0, Y, yt, ldy, st));
+  CUDA_TRY(multiply(x, tokens, in, ws, out, bias, 0, Y, yt, ldy, false, st));
   return GPTQ_OK;
 }
 
@@ -452,7 +508,7 @@ gptq_status_t matmul_int8_gated(const gptq_int8_tokens_t* x, int64_t tokens, int
                                 const gptq_int8_layer_t* up, int64_t out, int act, void* Y, gptq_dtype_t yt,
                                 int64_t ldy, cudaStream_t st) {
   const gptq_int8_layer_t* const ws[2] = {gate, up};
-  CUDA_TRY(multiply(x, tokens, in, ws, out, nullptr, act, Y, yt, ldy, st));
+  CUDA_TRY(multiply(x, tokens, in, ws, out, nullptr, act, Y, yt, ldy, false, st));
   return GPTQ_OK;
 }
 
@@ -472,7 +528,7 @@ gptq_status_t linear_int8(const void* X, gptq_dtype_t xt, int64_t tokens, int64_
   const gptq_status_t s = quantize_tokens(X, xt, tokens, in, ldx, const_cast<int8_t*>(q.x.q), q.x.ldq,
                                           const_cast<float*>(q.x.scale), const_cast<int32_t*>(q.x.sum), st);
   if (s != GPTQ_OK) return s;
-  CUDA_TRY(multiply(&q.x, tokens, in, layers, out, bias, act, Y, yt, ldy, st));
+  CUDA_TRY(multiply(&q.x, tokens, in, layers, out, bias, act, Y, yt, ldy, true, st));
   return GPTQ_OK;
 }
 

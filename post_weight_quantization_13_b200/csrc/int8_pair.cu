@@ -153,6 +153,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
   const int pair = (int)blockIdx.x / 2;
+  grid_dependency_wait();  // what came before ran beside the set-up above
 
   if (warp == 0) {
     if (lane == 0) {
@@ -348,21 +349,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 template <int G, typename T>
-cudaError_t launch(const PairMaps& maps, const PairParams& kp, cudaStream_t st) {
+cudaError_t launch(const PairMaps& maps, const PairParams& kp, bool follows, cudaStream_t st) {
   const void* f = (const void*)int8_pair_kernel<G, T>;
   cudaError_t e = ensure_smem_limit(f, 232448);
   if (e != cudaSuccess) return e;
   const size_t smem = 1024 + (size_t)kp.stages * kp.stage_bytes + kStageOut + kVectors + 256;
-  int8_pair_kernel<G, T><<<2 * kp.pairs, kThreads, smem, st>>>(maps, kp);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * kp.pairs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = follows ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, int8_pair_kernel<G, T>, maps, kp);
   note_launch();
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t pair_int8(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const gptq_int8_layer_t* const (&w)[2],
-                      int64_t out, const float* bias, int act, void* Y, gptq_dtype_t yt, int64_t ldy, uint32_t* status,
-                      cudaStream_t st) {
+                      int64_t out, const float* bias, int act, void* Y, gptq_dtype_t yt, int64_t ldy, bool follows,
+                      uint32_t* status, cudaStream_t st) {
   const int G = w[1] ? 2 : 1;
   PairParams kp = {};
   kp.tscale = x->scale;
@@ -394,12 +405,12 @@ cudaError_t pair_int8(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, c
   for (int g = 0; g < G; ++g)
     if (!int8_map(&maps.w[g], w[g]->w, out, in, w[g]->ldw, kp.bn / 2)) return cudaErrorInvalidValue;
   if (G == 2)
-    return yt == GPTQ_F16    ? launch<2, __half>(maps, kp, st)
-           : yt == GPTQ_BF16 ? launch<2, __nv_bfloat16>(maps, kp, st)
-                             : launch<2, float>(maps, kp, st);
-  return yt == GPTQ_F16    ? launch<1, __half>(maps, kp, st)
-         : yt == GPTQ_BF16 ? launch<1, __nv_bfloat16>(maps, kp, st)
-                           : launch<1, float>(maps, kp, st);
+    return yt == GPTQ_F16    ? launch<2, __half>(maps, kp, follows, st)
+           : yt == GPTQ_BF16 ? launch<2, __nv_bfloat16>(maps, kp, follows, st)
+                             : launch<2, float>(maps, kp, follows, st);
+  return yt == GPTQ_F16    ? launch<1, __half>(maps, kp, follows, st)
+         : yt == GPTQ_BF16 ? launch<1, __nv_bfloat16>(maps, kp, follows, st)
+                           : launch<1, float>(maps, kp, follows, st);
 }
 
 }  // namespace gptq

@@ -1,4 +1,4 @@
-// 8-bit integer products for one to four tokens (decode), the plain one and
+// 8-bit integer products for one or two tokens (decode), the plain one and
 // the gated pair, taking the tokens in 8 bits or in 16/32 (then each block
 // quantizes them itself: one launch, no scratch).
 //
@@ -42,6 +42,7 @@ struct RowsParams {
   int yt;
   int64_t ldy;
   int tokens, out, in, act;
+  int rows;  // the most channels a block owns
   int vec;  // x's rows start on 16-byte boundaries
 };
 
@@ -158,6 +159,11 @@ __global__ void __launch_bounds__(kThreads, 2) int8_rows_kernel(const __grid_con
   __shared__ int tsum[T];
   __shared__ uint32_t exchange[kWarps][T];
   __shared__ int sums[2][kWarps][N];
+  // the block's channels' scales, zeros and bias: fetched once up front, since
+  // a load in a batch's epilogue would hold up the whole block for its latency
+  float* const wscale = (float*)(codes + (size_t)T * ((kp.in + kSlice - 1) / kSlice) * kThreads);  // [G][rows]
+  int* const wzero = (int*)(wscale + G * kp.rows);                                                  // [G][rows]
+  float* const bias = (float*)(wzero + G * kp.rows);                                                // [rows]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int steps = (kp.in + kSlice - 1) / kSlice;
@@ -178,6 +184,14 @@ __global__ void __launch_bounds__(kThreads, 2) int8_rows_kernel(const __grid_con
 
   int4 w[kLoads];
   load(w, 0, 0);  // in flight while the tokens are quantized
+  for (int i = threadIdx.x; i < n_end - n_begin; i += kThreads) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      wscale[g * kp.rows + i] = __ldg(kp.wscale[g] + n_begin + i);
+      wzero[g * kp.rows + i] = kp.wzero[g] ? __ldg(kp.wzero[g] + n_begin + i) : 0;
+    }
+    bias[i] = G == 1 && kp.bias ? __ldg(kp.bias + n_begin + i) : 0.f;
+  }
   if (kp.xt < 0) {
     if (threadIdx.x < T) {
       tscale[threadIdx.x] = threadIdx.x < kp.tokens ? kp.tscale[threadIdx.x] : 0.f;
@@ -230,13 +244,13 @@ __global__ void __launch_bounds__(kThreads, 2) int8_rows_kernel(const __grid_con
           int total = 0;
 #pragma unroll
           for (int v = 0; v < kWarps; ++v) total += sums[batch & 1][v][g * R * T + threadIdx.x];
-          y[g] = scaled(total, kp.wzero[g] ? __ldg(kp.wzero[g] + n) : 0, tsum[t], tscale[t], __ldg(kp.wscale[g] + n));
+          y[g] = scaled(total, wzero[g * kp.rows + n - n_begin], tsum[t], tscale[t], wscale[g * kp.rows + n - n_begin]);
         }
         float o = y[0];
         if (G == 2)
           o = activate(y[0], kp.act) * y[G - 1];
-        else if (kp.bias)
-          o += __ldg(kp.bias + n);
+        else
+          o += bias[n - n_begin];
         const int64_t at = t * kp.ldy + n;
         if (kp.yt == GPTQ_F16)
           ((__half*)kp.Y)[at] = from_f32<__half>(o);
@@ -250,14 +264,15 @@ __global__ void __launch_bounds__(kThreads, 2) int8_rows_kernel(const __grid_con
 }
 
 template <int G, int T>
-cudaError_t launch(const RowsParams& kp, cudaStream_t st, int sms) {
+cudaError_t launch(RowsParams& kp, cudaStream_t st, int sms) {
+  // two blocks an SM, none without a batch of its own
+  const int grid = std::min(2 * sms, (kp.out + kLoads / G - 1) / (kLoads / G));
+  kp.rows = (kp.out + grid - 1) / grid;
   const int steps = (kp.in + kSlice - 1) / kSlice;
-  const int smem = T * steps * kThreads * 16;
+  const int smem = T * steps * kThreads * 16 + (2 * G + 1) * kp.rows * 4;
   const void* f = (const void*)int8_rows_kernel<G, T>;
   cudaError_t e = ensure_smem_limit(f, smem);
   if (e != cudaSuccess) return e;
-  // two blocks an SM, none without a batch of its own
-  const int grid = std::min(2 * sms, (kp.out + kLoads / G - 1) / (kLoads / G));
   int8_rows_kernel<G, T><<<grid, kThreads, smem, st>>>(kp);
   note_launch();
   return cudaGetLastError();
@@ -293,10 +308,8 @@ cudaError_t rows_int8(const void* x, int xt, int64_t ldx, const gptq_int8_tokens
   kp.act = act;
   kp.vec = (uintptr_t)kp.x % 16 == 0 && (kp.ldx * (xt == GPTQ_F32 ? 4 : 2)) % 16 == 0;
   const int sms = device_info().sms;
-  if (w[1]) return tokens == 1 ? launch<2, 1>(kp, st, sms) : tokens == 2 ? launch<2, 2>(kp, st, sms)
-                                                                         : launch<2, 4>(kp, st, sms);
-  return tokens == 1 ? launch<1, 1>(kp, st, sms) : tokens == 2 ? launch<1, 2>(kp, st, sms)
-                                                               : launch<1, 4>(kp, st, sms);
+  if (w[1]) return tokens == 1 ? launch<2, 1>(kp, st, sms) : launch<2, 2>(kp, st, sms);
+  return tokens == 1 ? launch<1, 1>(kp, st, sms) : launch<1, 2>(kp, st, sms);
 }
 
 }  // namespace gptq

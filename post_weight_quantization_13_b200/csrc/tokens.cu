@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(1024) quantize_tokens_kernel(const T* __restri
                                                                float* __restrict__ scale, int32_t* __restrict__ sum,
                                                                bool vec) {
   __shared__ uint32_t buf[64];
+  grid_launch_dependents();  // a product behind this kernel sets up beside it
   const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= tokens) return;  // whole warps: rows of several per block are one warp wide
   RowReduce red(buf);
