@@ -6,6 +6,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace gptq {
@@ -28,38 +30,60 @@ __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2hal
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-// Eight consecutive elements as loaded; left elements (>= 1) lie inside the
-// row, those past its end read as zero.  vec: the address is 16-byte aligned.
+// Eight consecutive elements as loaded, in 32-bit words.
 template <typename T>
 struct Raw8 {
-  alignas(16) T v[8];
+  alignas(16) uint32_t w[2 * sizeof(T)];
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(w[i]);
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    } else {
+      return __half2float(__ushort_as_half((unsigned short)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu)));
+    }
+  }
 };
+template <typename T>
+__device__ __forceinline__ Raw8<T> zero8() {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < 2 * (int)sizeof(T); ++i) r.w[i] = 0u;
+  return r;
+}
+// The `left` (>= 1) first of eight elements lie inside the row, the others
+// read as zero.  vec: the address is 16-byte aligned.
 template <typename T>
 __device__ __forceinline__ Raw8<T> load8(const T* __restrict__ p, int left, bool vec) {
   Raw8<T> r;
   if (vec && left >= 8) {
 #pragma unroll
     for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-      reinterpret_cast<uint4*>(r.v)[i] = reinterpret_cast<const uint4*>(p)[i];
-  } else {
+      reinterpret_cast<uint4*>(r.w)[i] = reinterpret_cast<const uint4*>(p)[i];
+  } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r.v[i] = i < left ? p[i] : from_f32<T>(0.f);
+    for (int i = 0; i < 8; ++i) r.w[i] = i < left ? reinterpret_cast<const uint32_t*>(p)[i] : 0u;
+  } else {
+    const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r.w[i] = (2 * i < left ? (uint32_t)h[2 * i] : 0u) | (2 * i + 1 < left ? (uint32_t)h[2 * i + 1] << 16 : 0u);
   }
   return r;
 }
 template <typename T>
 __device__ __forceinline__ void store8(T* __restrict__ p, const float* v, int left, bool vec) {
-  Raw8<T> r;
+  alignas(16) T r[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r.v[i] = from_f32<T>(v[i]);
+  for (int i = 0; i < 8; ++i) r[i] = from_f32<T>(v[i]);
   if (vec && left >= 8) {
 #pragma unroll
     for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-      reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(r.v)[i];
+      reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(r)[i];
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < left) p[i] = r.v[i];
+      if (i < left) p[i] = r[i];
   }
 }
 
@@ -85,12 +109,34 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
 }
 
 // ------------------------------------------------------------ token quantizer
+// The largest magnitude of a row is taken on the bit patterns, where NaN and
+// infinity sort above every finite value.  16-bit types: both halves of a
+// word at once; magnitude_bits turns the running maximum into the bits of the
+// fp32 value.
+template <typename T>
+__device__ __forceinline__ uint32_t magnitude(const Raw8<T>& r, uint32_t top) {
+#pragma unroll
+  for (int i = 0; i < 2 * (int)sizeof(T); ++i)
+    top = sizeof(T) == 2 ? __vmaxu2(top, r.w[i] & 0x7fff7fffu) : max(top, r.w[i] & 0x7fffffffu);
+  return top;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t magnitude_bits(uint32_t top) {
+  if (sizeof(T) == 4) return top;
+  const unsigned short h = (unsigned short)max(top & 0xffffu, top >> 16);
+  return __float_as_uint(to_f32(*reinterpret_cast<const T*>(&h)));
+}
+
 // s = RN(max |x| RN(1/127)), code = clamp(rint(RN(x / s)), -127, 127), fp32.
-// top: the bit pattern of the row's largest magnitude, where NaN and infinity
-// sort above every finite value and give s = NaN and codes of zero.  The
-// quotient comes from quot_rn (five operations instead of a divide) while s
-// is in its range; an x too small for that range has |x / s| < 1/2 either
-// way, its code is 0.
+// A row with NaN or an infinity gets s = NaN and codes of zero.
+//
+// Eight codes at a time: c = rint(x y) with y = RN(1/s), by adding and taking
+// off 1.5 2^23, which leaves the code in the sum's low byte.  x y and RN(x/s)
+// are both within 127 2^-24 of x / s, so they can only round apart where x y
+// is within 2^-14 of a halfway case; those eight are redone with the exact
+// quotient (quot_rn, or a division where s is out of its range).  |x y| stays
+// below 127.5, so nothing needs clamping there.  About 5 operations a value;
+// the exact quotient for all took 16.
 struct TokenScale {
   float scale, inv;
   bool some, fast;
@@ -101,10 +147,39 @@ struct TokenScale {
     fast = scale >= 0x1p-60f && scale <= 0x1p60f;
     inv = fast ? __frcp_rn(scale) : 0.f;
   }
-  __device__ __forceinline__ int code(float x) const {
-    if (!some) return 0;
+  __device__ __forceinline__ uint32_t code(float x) const {
     const int c = __float2int_rn(fast ? quot_rn(x, scale, inv) : __fdiv_rn(x, scale));
-    return min(127, max(-127, c));
+    return (uint32_t)min(127, max(-127, c));
+  }
+  static __device__ __forceinline__ uint32_t pack(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+  }
+  __device__ __forceinline__ uint2 codes(const float (&x)[8]) const {
+    if (!some) return make_uint2(0u, 0u);
+    uint32_t b[8];
+    float off = 1.f;
+    if (fast) {
+      off = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float m = fmaf(x[i], inv, 12582912.f);
+        b[i] = __float_as_uint(m);
+        off = fmaxf(off, fabsf(fmaf(x[i], inv, 12582912.f - m)));
+      }
+    }
+    if (off > 0.5f - 0x1p-14f) {
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        // (a rolled loop over registers: selects instead of indexing)
+        float v = x[0];
+#pragma unroll
+        for (int u = 1; u < 8; ++u) v = u == i ? x[u] : v;
+        const uint32_t c = code(v);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) b[u] = u == i ? c : b[u];
+      }
+    }
+    return make_uint2(pack(b[0], b[1], b[2], b[3]), pack(b[4], b[5], b[6], b[7]));
   }
 };
 

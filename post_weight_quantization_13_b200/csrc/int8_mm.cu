@@ -475,10 +475,10 @@ cudaError_t multiply(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, co
                      cudaStream_t st) {
   if (few(tokens)) return rows_int8(nullptr, 0, 0, x, tokens, in, w, out, bias, act, Y, yt, ldy, st);
   if (many(tokens)) {
-    void* status = nullptr;
-    const cudaError_t e = cudaGetSymbolAddress(&status, g_int8_status);
+    uint32_t* status = nullptr;
+    const cudaError_t e = int8_status_word(&status);
     if (e != cudaSuccess) return e;
-    return pair_int8(x, tokens, in, w, out, bias, act, Y, yt, ldy, follows, (uint32_t*)status, st);
+    return pair_int8(x, tokens, in, w, out, bias, act, Y, yt, ldy, follows, status, st);
   }
   if (w[1]) return run<2>(x, tokens, in, w, out, bias, act, Y, yt, ldy, follows, st);
   return run<1>(x, tokens, in, w, out, bias, act, Y, yt, ldy, follows, st);
@@ -532,14 +532,16 @@ gptq_status_t linear_int8(const void* X, gptq_dtype_t xt, int64_t tokens, int64_
   return GPTQ_OK;
 }
 
+cudaError_t int8_status_word(uint32_t** word) { return cudaGetSymbolAddress((void**)word, g_int8_status); }
+
 gptq_status_t int8_status(cudaStream_t st) {
   uint32_t status = 0;
-  void* at = nullptr;
-  CUDA_TRY(cudaGetSymbolAddress(&at, g_int8_status));
+  uint32_t* at = nullptr;
+  CUDA_TRY(int8_status_word(&at));
   CUDA_TRY(cudaMemcpyAsync(&status, at, sizeof(status), cudaMemcpyDeviceToHost, st));
   CUDA_TRY(cudaMemsetAsync(at, 0, sizeof(status), st));
   CUDA_TRY(cudaStreamSynchronize(st));
-  if (status & ST_TIMEOUT) return fail(GPTQ_ERR_TIMEOUT, "a bounded device-side wait gave up in an int8 product");
+  if (status & ST_TIMEOUT) return fail(GPTQ_ERR_TIMEOUT, "a bounded device-side wait gave up in an int8 kernel");
   return GPTQ_OK;
 }
 

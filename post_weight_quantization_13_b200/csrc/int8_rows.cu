@@ -87,17 +87,10 @@ __device__ __forceinline__ int warp_sums(int (&v)[N]) {
   return v[0];
 }
 
-// The 16 columns from k0 of token row x as fp32; columns past `in` are zero.
-template <typename T>
-__device__ __forceinline__ void load_columns(const T* __restrict__ x, int k0, int in, bool vec, float (&f)[16]) {
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int c = k0 + 8 * u;
-    Raw8<T> r;
-    if (c < in) r = load8(x + c, in - c, vec);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[8 * u + i] = c < in ? to_f32(r.v[i]) : 0.f;
-  }
+// Eight columns from c of a token's row; columns past `in` are zero.
+template <typename X>
+__device__ __forceinline__ Raw8<X> load_columns(const X* __restrict__ row, int c, int in, bool vec) {
+  return c < in ? load8(row + c, in - c, vec) : zero8<X>();
 }
 
 // The block's T tokens into codes (each thread its own columns), their scales
@@ -106,47 +99,45 @@ template <typename X, int T>
 __device__ __forceinline__ void quantize_block(const RowsParams& kp, int4* codes, int steps, float* tscale, int* tsum,
                                                uint32_t (*exchange)[T]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint32_t top[T];
+  const int chunks = 2 * steps;  // of eight columns
 #pragma unroll
   for (int t = 0; t < T; ++t) {
-    top[t] = 0u;
-    if (t >= kp.tokens) continue;
-    for (int s = 0; s < steps; ++s) {
-      float f[16];
-      load_columns((const X*)kp.x + t * kp.ldx, s * kSlice + 16 * (int)threadIdx.x, kp.in, kp.vec, f);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) top[t] = max(top[t], __float_as_uint(f[i]) & 0x7fffffffu);
+    uint32_t top = 0u;
+    if (t < kp.tokens) {
+#pragma unroll 4
+      for (int s = 0; s < chunks; ++s)
+        top = magnitude(load_columns((const X*)kp.x + t * kp.ldx, (s >> 1) * kSlice + 16 * (int)threadIdx.x + 8 * (s & 1),
+                                     kp.in, kp.vec), top);
     }
-    top[t] = __reduce_max_sync(0xffffffffu, top[t]);
-    if (lane == 0) exchange[warp][t] = top[t];
+    top = __reduce_max_sync(0xffffffffu, magnitude_bits<X>(top));
+    if (lane == 0) exchange[warp][t] = top;
   }
   if (threadIdx.x < T) tsum[threadIdx.x] = 0;
   __syncthreads();
 #pragma unroll
   for (int t = 0; t < T; ++t) {
+    uint32_t top = 0u;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = max(top, exchange[w][t]);
+    const TokenScale scale(top);
     int total = 0;
-    if (t < kp.tokens) {
+#pragma unroll 2
+    for (int s = 0; s < chunks; ++s) {  // the second reading hits L1
+      uint2 c = make_uint2(0u, 0u);
+      if (t < kp.tokens) {
+        const Raw8<X> r = load_columns((const X*)kp.x + t * kp.ldx,
+                                       (s >> 1) * kSlice + 16 * (int)threadIdx.x + 8 * (s & 1), kp.in, kp.vec);
+        float f[8];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top[t] = max(top[t], exchange[w][t]);
-    }
-    const TokenScale s(top[t]);
-    for (int step = 0; step < steps; ++step) {
-      float f[16];
-      uint32_t v[4] = {0u, 0u, 0u, 0u};
-      if (t < kp.tokens) {  // the second reading hits L1
-        load_columns((const X*)kp.x + t * kp.ldx, step * kSlice + 16 * (int)threadIdx.x, kp.in, kp.vec, f);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int c = s.code(f[i]);
-          total += c;
-          v[i >> 2] |= (uint32_t)(c & 0xff) << (8 * (i & 3));
-        }
+        for (int i = 0; i < 8; ++i) f[i] = r.get(i);
+        c = scale.codes(f);
+        total = __dp4a((int)c.x, 0x01010101, __dp4a((int)c.y, 0x01010101, total));
       }
-      codes[(t * steps + step) * kThreads + threadIdx.x] = make_int4((int)v[0], (int)v[1], (int)v[2], (int)v[3]);
+      reinterpret_cast<uint2*>(codes + (t * steps + (s >> 1)) * kThreads + threadIdx.x)[s & 1] = c;
     }
     total = __reduce_add_sync(0xffffffffu, total);
     if (lane == 0) atomicAdd(&tsum[t], total);
-    if (threadIdx.x == 0) tscale[t] = s.scale;
+    if (threadIdx.x == 0) tscale[t] = scale.scale;
   }
 }
 
@@ -175,10 +166,20 @@ __global__ void __launch_bounds__(kThreads, 2) int8_rows_kernel(const __grid_con
   // the range repeat its last one; their sums are not used.
   auto load = [&](int4 (&w)[kLoads], int batch, int step) {
     const int k = step * kSlice + 16 * (int)threadIdx.x;
+    const int n0 = n_begin + batch * R;
+    const int left = kp.in - k;
+    if (left >= 16 && n0 + R <= n_end) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int n = min(n_begin + batch * R + i % R, n_end - 1);
-      w[i] = k < kp.in ? load16(kp.w[i / R] + n * kp.ldw[i / R] + k, kp.in - k) : make_int4(0, 0, 0, 0);
+      for (int g = 0; g < G; ++g) {
+        const int8_t* p = kp.w[g] + n0 * kp.ldw[g] + k;
+#pragma unroll
+        for (int i = 0; i < R; ++i, p += kp.ldw[g]) w[g * R + i] = __ldg(reinterpret_cast<const int4*>(p));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        w[i] = left > 0 ? load16(kp.w[i / R] + min(n0 + i % R, n_end - 1) * kp.ldw[i / R] + k, left)
+                        : make_int4(0, 0, 0, 0);
     }
   };
 

@@ -105,6 +105,9 @@ cudaError_t pair_int8(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, c
 // boxes of box_rows rows by 128 bytes; what lies past the matrix reads as zero.
 bool int8_map(CUtensorMap* m, const int8_t* base, int64_t rows, int64_t in, int64_t ld, int box_rows);
 gptq_status_t int8_status(cudaStream_t st);
+// The current device's status word of these kernels, read and cleared by
+// int8_status.
+cudaError_t int8_status_word(uint32_t** word);
 // Checks of a workspace argument (abi.cu).
 gptq_status_t check_ws(void* ws, size_t ws_bytes, size_t need);
 

@@ -22,6 +22,16 @@
 namespace gptq {
 namespace {
 
+constexpr int kMaxStages = 8;            // of the streaming norm's ring
+constexpr int kSmemPerSm = 227 * 1024;
+
+// Chunk i of the thread's share of a row of d elements; zero past the end.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_chunk(const T* __restrict__ row, int i, int d, bool vec) {
+  const int c0 = 8 * (threadIdx.x + i * blockDim.x);
+  return c0 < d ? load8(row + c0, d - c0, vec) : zero8<T>();
+}
+
 // ------------------------------------------------------------ row reductions
 // Reductions over the threads of one row (blockDim.x of them).  Successive
 // reductions of a wide row alternate between two exchange buffers, so one
@@ -58,37 +68,26 @@ struct RowReduce {
   }
 };
 
-// The token quantizer on a row in registers (TokenScale holds its arithmetic).  The largest magnitude is taken on the bit patterns, where
-// NaN and infinity sort above every finite value; such a row gets s = NaN and
-// codes of zero, so its product row is NaN and no other row is touched.
+// A row in registers, top its largest magnitude (fp32 bits) over this thread's
+// elements, to codes, scale and sum.
 template <int NV>
-__device__ __forceinline__ void quantize_row(const float (&v)[NV][8], int d, RowReduce& red, int8_t* __restrict__ q,
-                                             float* __restrict__ scale, int32_t* __restrict__ sum) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int u = 0; u < 8; ++u) top = max(top, __float_as_uint(v[i][u]) & 0x7fffffffu);
-  top = red.max_u32(top);
-  const TokenScale s(top);
+__device__ __forceinline__ void quantize_row(const float (&v)[NV][8], uint32_t top, int d, RowReduce& red,
+                                             int8_t* __restrict__ q, float* __restrict__ scale,
+                                             int32_t* __restrict__ sum) {
+  const TokenScale s(red.max_u32(top));
   int total = 0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c0 = 8 * (threadIdx.x + i * blockDim.x);
     if (c0 >= d) continue;
-    uint32_t w[2] = {0u, 0u};
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int code = s.code(v[i][u]);
-      total += code;
-      w[u >> 2] |= (uint32_t)(code & 0xff) << (8 * (u & 3));
-    }
+    const uint2 w = s.codes(v[i]);
+    total = __dp4a((int)w.x, 0x01010101, __dp4a((int)w.y, 0x01010101, total));
     if (c0 + 8 <= d) {
-      *reinterpret_cast<uint2*>(q + c0) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(q + c0) = w;
     } else {
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        if (c0 + u < d) q[c0 + u] = (int8_t)(w[u >> 2] >> (8 * (u & 3)));
+        if (c0 + u < d) q[c0 + u] = (int8_t)((u < 4 ? w.x : w.y) >> (8 * (u & 3)));
     }
   }
   total = red.sum_s32(total);
@@ -109,15 +108,17 @@ __global__ void __launch_bounds__(1024) quantize_tokens_kernel(const T* __restri
   if (t >= tokens) return;  // whole warps: rows of several per block are one warp wide
   RowReduce red(buf);
   float v[NV][8];
+  uint32_t top = 0;
+  Raw8<T> r[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) r[i] = load_chunk(X + t * ldx, i, d, vec);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c0 = 8 * (threadIdx.x + i * blockDim.x);
-    Raw8<T> r;
-    if (c0 < d) r = load8(X + t * ldx + c0, d - c0, vec);
+    top = magnitude(r[i], top);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[i][u] = c0 < d ? to_f32(r.v[u]) : 0.f;
+    for (int u = 0; u < 8; ++u) v[i][u] = r[i].get(u);
   }
-  quantize_row<NV>(v, d, red, q + t * ldq, scale + t, sum + t);
+  quantize_row<NV>(v, magnitude_bits<T>(top), d, red, q + t * ldq, scale + t, sum + t);
 }
 
 // ------------------------------------------------------------------- norms
@@ -132,16 +133,40 @@ struct NormParams {
   int32_t* sum;
   float alpha, beta, eps;
   int layer;
+  int stages, stage_bytes;  // of the streaming kernel
+  uint32_t* status;
   // 16-byte access per operand
   int vec_h, vec_y, vec_post_weight, vec_post_bias, vec_gate, vec_weight, vec_bias, vec_h_out, vec_x;
 };
 
-// v <- norm(v) * weight (+ bias) over the row's d elements.
+// A norm's weight and bias (or a gate) at the thread's columns.  A row of up to
+// two chunks a thread fetches them with the row itself, so that no load waits
+// behind a statistic; wider rows fetch them where they are used, for want of
+// registers.
+template <typename T, int NV>
+struct Vector {
+  static constexpr bool kEarly = NV <= 2;
+  const T* p;
+  int d, vec;
+  Raw8<T> r[kEarly ? NV : 1];
+  __device__ __forceinline__ Vector(const void* p_, int d_, int vec_) : p((const T*)p_), d(d_), vec(vec_) {
+    if (kEarly && p) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) r[kEarly ? i : 0] = load_chunk(p, i, d, vec);
+    }
+  }
+  __device__ __forceinline__ explicit operator bool() const { return p != nullptr; }
+  __device__ __forceinline__ Raw8<T> chunk(int i) const {
+    return kEarly ? r[kEarly ? i : 0] : load_chunk(p, i, d, vec);
+  }
+};
+
+// v <- norm(v) * weight (+ bias) over the row's d elements; elements past its
+// end are zero before and after.
 template <typename T, int NV>
 __device__ __forceinline__ void norm_row(float (&v)[NV][8], const NormParams& p, RowReduce& red,
-                                         const T* __restrict__ w, const T* __restrict__ b, int vec_w, int vec_b) {
-  const int d = p.d;
-  const float inv_d = 1.f / (float)d;
+                                         const Vector<T, NV>& w, const Vector<T, NV>& b) {
+  const float inv_d = 1.f / (float)p.d;
   if (p.layer) {
     float s = 0.f;
 #pragma unroll
@@ -154,7 +179,7 @@ __device__ __forceinline__ void norm_row(float (&v)[NV][8], const NormParams& p,
       const int c0 = 8 * (threadIdx.x + i * blockDim.x);
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        if (c0 + u < d) v[i][u] -= mean;  // elements past the end stay zero
+        if (c0 + u < p.d) v[i][u] -= mean;
     }
   }
   float s2 = 0.f;
@@ -165,84 +190,82 @@ __device__ __forceinline__ void norm_row(float (&v)[NV][8], const NormParams& p,
   const float r = rsqrtf(fmaf(red.sum(s2), inv_d, p.eps));
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c0 = 8 * (threadIdx.x + i * blockDim.x);
-    if (c0 >= d) continue;
-    const Raw8<T> rw = load8(w + c0, d - c0, vec_w);
+    const Raw8<T> rw = w.chunk(i);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[i][u] = v[i][u] * r * to_f32(rw.v[u]);
+    for (int u = 0; u < 8; ++u) v[i][u] = v[i][u] * r * rw.get(u);
     if (b) {
-      const Raw8<T> rb = load8(b + c0, d - c0, vec_b);
+      const Raw8<T> rb = b.chunk(i);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[i][u] += to_f32(rb.v[u]);
+      for (int u = 0; u < 8; ++u) v[i][u] += rb.get(u);
     }
   }
 }
 
-// h' = alpha h + beta gate * post(y);  x = pre(h') in 16/32 bits and/or int8.
-// The pre-norm works on h' before it is rounded to its stored type.
-template <typename T, typename H, int NV>
-__global__ void __launch_bounds__(1024) norm_tokens_kernel(const __grid_constant__ NormParams p) {
-  __shared__ uint32_t buf[64];
-  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  if (t >= p.tokens) return;
-  const int d = p.d;
-  RowReduce red(buf);
-  float v[NV][8];
-  Raw8<H> hr[NV];
-  const H* __restrict__ h = (const H*)p.h + t * p.ldh;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {  // both operands' loads are in flight together
-    const int c0 = 8 * (threadIdx.x + i * blockDim.x);
-    if (c0 < d) {
-      hr[i] = load8(h + c0, d - c0, p.vec_h);
-    } else {
-#pragma unroll
-      for (int u = 0; u < 8; ++u) hr[i].v[u] = from_f32<H>(0.f);
-    }
-  }
-  if (p.y) {
-    const T* __restrict__ y = (const T*)p.y + t * p.ldy;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c0 = 8 * (threadIdx.x + i * blockDim.x);
-      Raw8<T> r;
-      if (c0 < d) r = load8(y + c0, d - c0, p.vec_y);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) v[i][u] = c0 < d ? to_f32(r.v[u]) : 0.f;
-    }
-    if (p.post_weight)
-      norm_row<T, NV>(v, p, red, (const T*)p.post_weight, (const T*)p.post_bias, p.vec_post_weight, p.vec_post_bias);
-    if (p.gate) {
-      const T* __restrict__ g = (const T*)p.gate + t * p.ldgate;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c0 = 8 * (threadIdx.x + i * blockDim.x);
-        if (c0 >= d) continue;
-        const Raw8<T> r = load8(g + c0, d - c0, p.vec_gate);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) v[i][u] *= to_f32(r.v[u]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int u = 0; u < 8; ++u) v[i][u] = fmaf(p.alpha, to_f32(hr[i].v[u]), p.beta * v[i][u]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int u = 0; u < 8; ++u) v[i][u] = p.alpha * to_f32(hr[i].v[u]);
-  }
+// Zero past the row's end: 0 * inf must not reach a statistic.
+template <int NV>
+__device__ __forceinline__ void clear_past(float (&v)[NV][8], int d) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c0 = 8 * (threadIdx.x + i * blockDim.x);
+    if (c0 + 8 <= d) continue;
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-      if (c0 + u >= d) v[i][u] = 0.f;  // a bias or 0 * inf must not reach the statistics
-    if (p.h_out && c0 < d) store8((H*)p.h_out + t * p.ldh_out + c0, v[i], d - c0, p.vec_h_out);
+      if (c0 + u >= d) v[i][u] = 0.f;
+  }
+}
+
+// One token: h' = alpha h + beta gate * post(y);  x = pre(h') in 16/32 bits
+// and/or int8.  The pre-norm works on h' before it is rounded to its stored
+// type.  h(i), y(i) and gate(i) give the operands' chunks; release() is called
+// once by every thread when the whole row has been read by all of them.
+template <typename T, typename H, int NV, typename LoadH, typename LoadY, typename LoadGate, typename Release>
+__device__ __forceinline__ void norm_token(const NormParams& p, int64_t t, RowReduce& red, LoadH h, LoadY y,
+                                           LoadGate gate, const Vector<T, NV>& post_weight,
+                                           const Vector<T, NV>& post_bias, const Vector<T, NV>& weight,
+                                           const Vector<T, NV>& bias, Release release) {
+  const int d = p.d;
+  float v[NV][8];
+  if (p.y) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const Raw8<T> r = y(i);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[i][u] = r.get(u);
+    }
+    if (post_weight) norm_row<T, NV>(v, p, red, post_weight, post_bias);
+    if (p.gate) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const Raw8<T> r = gate(i);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[i][u] *= r.get(u);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const Raw8<H> r = h(i);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[i][u] = fmaf(p.alpha, r.get(u), p.beta * v[i][u]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const Raw8<H> r = h(i);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[i][u] = p.alpha * r.get(u);
+    }
+  }
+  clear_past(v, d);
+  if (p.h_out) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c0 = 8 * (threadIdx.x + i * blockDim.x);
+      if (c0 < d) store8((H*)p.h_out + t * p.ldh_out + c0, v[i], d - c0, p.vec_h_out);
+    }
   }
   if (!p.weight) return;
-  norm_row<T, NV>(v, p, red, (const T*)p.weight, (const T*)p.bias, p.vec_weight, p.vec_bias);
+  norm_row<T, NV>(v, p, red, weight, bias);
+  release();
   if (p.x) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -251,14 +274,99 @@ __global__ void __launch_bounds__(1024) norm_tokens_kernel(const __grid_constant
     }
   }
   if (p.q) {
+    clear_past(v, d);
+    uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c0 = 8 * (threadIdx.x + i * blockDim.x);
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (c0 + u >= d) v[i][u] = 0.f;
+      for (int u = 0; u < 8; ++u) top = max(top, __float_as_uint(v[i][u]) & 0x7fffffffu);
+    quantize_row<NV>(v, top, d, red, p.q + t * p.ldq, p.scale + t, p.sum + t);
+  }
+}
+
+// A row a warp or a block, every operand straight to registers: few tokens,
+// narrow rows, unaligned rows.
+template <typename T, typename H, int NV>
+__global__ void __launch_bounds__(1024) norm_tokens_kernel(const __grid_constant__ NormParams p) {
+  __shared__ uint32_t buf[64];
+  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (t >= p.tokens) return;
+  const int d = p.d;
+  RowReduce red(buf);
+  Raw8<H> h[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) h[i] = load_chunk((const H*)p.h + t * p.ldh, i, d, p.vec_h);
+  const Vector<T, NV> y(p.y ? (const T*)p.y + t * p.ldy : nullptr, d, p.vec_y);
+  const Vector<T, NV> gate(p.gate ? (const T*)p.gate + t * p.ldgate : nullptr, d, p.vec_gate);
+  const Vector<T, NV> post_weight(p.post_weight, d, p.vec_post_weight), post_bias(p.post_bias, d, p.vec_post_bias);
+  const Vector<T, NV> weight(p.weight, d, p.vec_weight), bias(p.bias, d, p.vec_bias);
+  norm_token<T, H, NV>(
+      p, t, red, [&](int i) { return h[i]; }, [&](int i) { return y.chunk(i); }, [&](int i) { return gate.chunk(i); },
+      post_weight, post_bias, weight, bias, [] {});
+}
+
+// Many tokens of wide, aligned rows: persistent blocks whose rows arrive in a
+// ring of shared-memory stages by bulk copies, the next rows' while this one
+// is worked on, so memory is never waiting for a statistic.  The weights stay
+// in registers for all of a block's rows.
+template <typename T, typename H, int NV, int MaxThreads>
+__global__ void __launch_bounds__(MaxThreads) norm_stream_kernel(const __grid_constant__ NormParams p) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint32_t buf[64];
+  __shared__ uint64_t full[kMaxStages];
+  const int d = p.d, stages = p.stages;
+  const uint32_t hb = (uint32_t)(d * sizeof(H)), tb = (uint32_t)(d * sizeof(T));
+  const bool gates = p.gate && p.ldgate;  // a gate for each token comes with the row
+  const uint32_t bytes = hb + (p.y ? tb : 0u) + (gates ? tb : 0u);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  auto fetch = [&](int64_t t, int s) {  // one thread
+    uint8_t* at = ring + (size_t)s * p.stage_bytes;
+    mbar_arrive_expect_tx(&full[s], bytes);
+    bulk_load(at, (const H*)p.h + t * p.ldh, hb, &full[s]);
+    at += hb;
+    if (p.y) {
+      bulk_load(at, (const T*)p.y + t * p.ldy, tb, &full[s]);
+      at += tb;
     }
-    quantize_row<NV>(v, d, red, p.q + t * p.ldq, p.scale + t, p.sum + t);
+    if (gates) bulk_load(at, (const T*)p.gate + t * p.ldgate, tb, &full[s]);
+  };
+  if (threadIdx.x == 0)
+    for (int s = 0; s < stages; ++s) {
+      const int64_t t = blockIdx.x + (int64_t)s * gridDim.x;
+      if (t < p.tokens) fetch(t, s);
+    }
+  RowReduce red(buf);
+  const Vector<T, NV> post_weight(p.post_weight, d, 1), post_bias(p.post_bias, d, 1);
+  const Vector<T, NV> weight(p.weight, d, 1), bias(p.bias, d, 1);
+  const Vector<T, NV> gate(p.gate && !gates ? p.gate : nullptr, d, 1);
+  int s = 0;
+  uint32_t phase = 0;
+  bool gave_up = false;  // after a wait that gave up the block runs on without waiting, on whatever is there
+  for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
+    if (!gave_up && !mbar_wait(&full[s], phase)) {
+      gave_up = true;
+      raise_status(p.status, ST_TIMEOUT);
+    }
+    const uint8_t* at = ring + (size_t)s * p.stage_bytes;
+    const H* h = (const H*)at;
+    const T* y = (const T*)(at + hb);
+    const T* g = y + (p.y ? d : 0);
+    norm_token<T, H, NV>(
+        p, t, red, [&](int i) { return load_chunk(h, i, d, true); }, [&](int i) { return load_chunk(y, i, d, true); },
+        [&](int i) { return gates ? load_chunk(g, i, d, true) : gate.chunk(i); }, post_weight, post_bias, weight, bias,
+        [&] {
+          // the barrier of the pre-norm's statistic lies behind every read
+          const int64_t next = t + (int64_t)stages * gridDim.x;
+          if (threadIdx.x == 0 && next < p.tokens) fetch(next, s);
+        });
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1;
+    }
   }
 }
 
@@ -311,9 +419,9 @@ dim3 row_block(int d, int nv) {
   return lanes <= 32 ? dim3(32, 4) : dim3((unsigned)((lanes + 31) / 32 * 32), 1);
 }
 
-// Chunks a thread: two, so that a row of 4096 is a block of 256; four beyond
-// 16384 elements, where 1024 threads hold no more with two.
-int row_chunks(int d) { return d > 1024 * 16 ? 4 : 2; }
+// Chunks a thread.  One as long as 1024 threads then hold the row: narrow
+// threads leave room for the most rows in flight.  Beyond that two, then four.
+int row_chunks(int d) { return d <= 1024 * 8 ? 1 : d <= 1024 * 16 ? 2 : 4; }
 
 template <typename T>
 cudaError_t launch_quantize(const T* X, int64_t tokens, int d, int64_t ldx, int8_t* q, int64_t ldq, float* scale,
@@ -322,7 +430,9 @@ cudaError_t launch_quantize(const T* X, int64_t tokens, int d, int64_t ldx, int8
   const int nv = row_chunks(d);
   const dim3 block = row_block(d, nv);
   const unsigned grid = (unsigned)((tokens + block.y - 1) / block.y);
-  if (nv == 2)
+  if (nv == 1)
+    quantize_tokens_kernel<T, 1><<<grid, block, 0, st>>>(X, tokens, d, ldx, q, ldq, scale, sum, vec);
+  else if (nv == 2)
     quantize_tokens_kernel<T, 2><<<grid, block, 0, st>>>(X, tokens, d, ldx, q, ldq, scale, sum, vec);
   else
     quantize_tokens_kernel<T, 4><<<grid, block, 0, st>>>(X, tokens, d, ldx, q, ldq, scale, sum, vec);
@@ -330,17 +440,53 @@ cudaError_t launch_quantize(const T* X, int64_t tokens, int d, int64_t ldx, int8
   return cudaGetLastError();
 }
 
+// Whether the streaming kernel takes the call: rows a block wide whose bytes
+// bulk copies can move (16-byte addresses and sizes; a vector's loads too),
+// and enough of them to fill every block's ring more than once.
 template <typename T, typename H>
-cudaError_t launch_norm(const NormParams& p, cudaStream_t st) {
-  const int nv = row_chunks(p.d);
-  const dim3 block = row_block(p.d, nv);
-  const unsigned grid = (unsigned)((p.tokens + block.y - 1) / block.y);
-  if (nv == 2)
-    norm_tokens_kernel<T, H, 2><<<grid, block, 0, st>>>(p);
-  else
-    norm_tokens_kernel<T, H, 4><<<grid, block, 0, st>>>(p);
+bool streams(const NormParams& p, int sms) {
+  return p.weight && p.d > 32 * 8 && p.d % 8 == 0 && p.tokens > 4 * sms && p.vec_h && (!p.y || p.vec_y) &&
+         (!p.gate || p.vec_gate) && p.vec_weight && (!p.bias || p.vec_bias) && (!p.post_weight || p.vec_post_weight) &&
+         (!p.post_bias || p.vec_post_bias);
+}
+
+template <typename T, typename H, int NV, int MaxThreads>
+cudaError_t launch_stream(const NormParams& p, dim3 block, int blocks, cudaStream_t st) {
+  const int smem = p.stages * p.stage_bytes;
+  const cudaError_t e = ensure_smem_limit((const void*)norm_stream_kernel<T, H, NV, MaxThreads>, smem);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)std::min<int64_t>(p.tokens, (int64_t)blocks * device_info().sms);
+  norm_stream_kernel<T, H, NV, MaxThreads><<<grid, block, smem, st>>>(p);
   note_launch();
   return cudaGetLastError();
+}
+
+template <typename T, typename H, int NV>
+cudaError_t launch_norm_nv(NormParams& p, cudaStream_t st) {
+  const dim3 block = row_block(p.d, NV);
+  if (block.y == 1 && streams<T, H>(p, device_info().sms)) {
+    p.stage_bytes = (int)round_up(p.d * (int)(sizeof(H) + (p.y ? sizeof(T) : 0) + (p.gate && p.ldgate ? sizeof(T) : 0)),
+                                  128);
+    // as many blocks as 64 registers a thread allow, their rings sharing the SM
+    const int blocks = std::max(1, 1024 / (int)block.x);
+    p.stages = std::min(kMaxStages, (kSmemPerSm / blocks - 2048) / p.stage_bytes);
+    if (p.stages >= 2) {
+      if constexpr (NV == 2)  // 85 registers hold a norm's vectors where 64 spill
+        if (block.x <= 768) return launch_stream<T, H, NV, 768>(p, block, blocks, st);
+      return launch_stream<T, H, NV, 1024>(p, block, blocks, st);
+    }
+  }
+  norm_tokens_kernel<T, H, NV><<<(unsigned)((p.tokens + block.y - 1) / block.y), block, 0, st>>>(p);
+  note_launch();
+  return cudaGetLastError();
+}
+
+template <typename T, typename H>
+cudaError_t launch_norm(NormParams& p, cudaStream_t st) {
+  const int nv = row_chunks(p.d);
+  return nv == 1   ? launch_norm_nv<T, H, 1>(p, st)
+         : nv == 2 ? launch_norm_nv<T, H, 2>(p, st)
+                   : launch_norm_nv<T, H, 4>(p, st);
 }
 
 int aligned_rows(const void* p, int64_t ld, gptq_dtype_t t) {
@@ -374,6 +520,7 @@ gptq_status_t quantize_tokens(const void* X, gptq_dtype_t xt, int64_t tokens, in
 
 gptq_status_t norm_tokens(const gptq_norm_t* a, cudaStream_t st) {
   NormParams p = {};
+  CUDA_TRY(int8_status_word(&p.status));
   p.tokens = a->tokens;
   p.d = (int)a->d;
   p.h = a->h;

@@ -207,6 +207,11 @@ NORMS = [  # tokens, d, type, residual type, kind, post, gate, alpha, beta, pad
     (33, 513, F16, F32, "layer", False, "channel", 1.0, 1.0, 3), (7, 4096, F16, F16, "layer", True, None, 1.0, 1.0, 0),
     (9, 11008, BF16, F32, "layer", True, "token", 0.7, 1.0, 0), (3, 16384, F32, F32, "rms", True, "token", 1.0, 1.0, 0),
     (2, 16392, BF16, BF16, "layer", True, "channel", 1.0, -1.0, 0), (2, 32768, F32, F32, "layer", True, "token", 1, 1, 0),
+    # many rows: the streaming kernel's rings go round, with and without a gate for each token, and with a tail
+    (1500, 512, BF16, BF16, "rms", True, "channel", 1.0, 0.5, 0), (5000, 264, F16, F32, "layer", True, "token", 1, 1, 8),
+    (1203, 11008, F16, F32, "layer", True, "token", 0.7, 1.0, 0), (700, 16384, BF16, BF16, "rms", False, None, 1, 1, 0),
+    (601, 32768, BF16, F32, "rms", True, "channel", 1, 1, 0), (999, 4096, F32, F32, "rms", True, "token", 1, 1, 0),
+    (2000, 4100, BF16, BF16, "rms", True, "channel", 1, 1, 0),
     (1001, 300, F16, F32, "rms", True, "channel", 1.0, 1.0, 1), (3, 32767, F16, F16, "rms", False, "token", 0.0, 1.0, 0),
 ]
 
