@@ -30,6 +30,49 @@ __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2hal
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
+// Two fp32 values in one 64-bit register pair: an operation on both is one
+// instruction (f32x2, sm_100), and these kernels are bound by issuing them.
+struct Pair {
+  uint64_t v;
+  Pair() = default;
+  __device__ __forceinline__ Pair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ explicit Pair(float a) : Pair(a, a) {}
+  __device__ __forceinline__ float2 f() const {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+  }
+};
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
+// N (even) values rounded to T, two at a time.
+template <int N, typename T>
+__device__ __forceinline__ void round_n(const float* v, T* r) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    if constexpr (std::is_same<T, __half>::value)
+      *reinterpret_cast<__half2*>(r + i) = __floats2half2_rn(v[i], v[i + 1]);
+    else if constexpr (std::is_same<T, __nv_bfloat16>::value)
+      *reinterpret_cast<__nv_bfloat162*>(r + i) = __floats2bfloat162_rn(v[i], v[i + 1]);
+    else
+      r[i] = v[i], r[i + 1] = v[i + 1];
+  }
+}
+
 // Eight consecutive elements as loaded, in 32-bit words.
 template <typename T>
 struct Raw8 {
@@ -44,6 +87,16 @@ struct Raw8 {
     }
   }
 };
+// Elements 2i and 2i + 1.
+template <typename T>
+__device__ __forceinline__ Pair get2(const Raw8<T>& r, int i) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r.w[i]));
+    return Pair(f.x, f.y);
+  } else {
+    return Pair(r.get(2 * i), r.get(2 * i + 1));
+  }
+}
 template <typename T>
 __device__ __forceinline__ Raw8<T> zero8() {
   Raw8<T> r;
@@ -71,11 +124,16 @@ __device__ __forceinline__ Raw8<T> load8(const T* __restrict__ p, int left, bool
   }
   return r;
 }
+// Eight values rounded to T; those from `left` on lie past the row's end.
 template <typename T>
-__device__ __forceinline__ void store8(T* __restrict__ p, const float* v, int left, bool vec) {
+__device__ __forceinline__ void store8(T* __restrict__ p, const Pair (&v)[4], int left, bool vec) {
   alignas(16) T r[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r[i] = from_f32<T>(v[i]);
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = v[i].f();
+    const float a[2] = {f.x, f.y};
+    round_n<2>(a, r + 2 * i);
+  }
   if (vec && left >= 8) {
 #pragma unroll
     for (int i = 0; i < (int)sizeof(T) / 2; ++i)
@@ -130,13 +188,13 @@ __device__ __forceinline__ uint32_t magnitude_bits(uint32_t top) {
 // s = RN(max |x| RN(1/127)), code = clamp(rint(RN(x / s)), -127, 127), fp32.
 // A row with NaN or an infinity gets s = NaN and codes of zero.
 //
-// Eight codes at a time: c = rint(x y) with y = RN(1/s), by adding and taking
-// off 1.5 2^23, which leaves the code in the sum's low byte.  x y and RN(x/s)
-// are both within 127 2^-24 of x / s, so they can only round apart where x y
-// is within 2^-14 of a halfway case; those eight are redone with the exact
-// quotient (quot_rn, or a division where s is out of its range).  |x y| stays
-// below 127.5, so nothing needs clamping there.  About 5 operations a value;
-// the exact quotient for all took 16.
+// Eight codes at a time: the quotient rounded to nearest by quot_rn's five
+// operations (an x too small for its range has |x / s| < 1/2 either way, its
+// code is 0), then rint by adding 1.5 2^23, which leaves the code in the sum's
+// low byte; |x / s| stays below 127.5, so nothing needs clamping.  A cheaper
+// rint(x RN(1/s)) with the exact quotient only near halfway cases does not
+// pay: 16-bit values over a 16-bit maximum fall exactly on them too often
+// (half a percent of bf16 values).
 struct TokenScale {
   float scale, inv;
   bool some, fast;
@@ -147,36 +205,29 @@ struct TokenScale {
     fast = scale >= 0x1p-60f && scale <= 0x1p60f;
     inv = fast ? __frcp_rn(scale) : 0.f;
   }
-  __device__ __forceinline__ uint32_t code(float x) const {
-    const int c = __float2int_rn(fast ? quot_rn(x, scale, inv) : __fdiv_rn(x, scale));
-    return (uint32_t)min(127, max(-127, c));
-  }
   static __device__ __forceinline__ uint32_t pack(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
   }
-  __device__ __forceinline__ uint2 codes(const float (&x)[8]) const {
-    if (!some) return make_uint2(0u, 0u);
+  __device__ __forceinline__ uint2 codes(const Pair (&x)[4]) const {
     uint32_t b[8];
-    float off = 1.f;
     if (fast) {
-      off = 0.f;
+      const Pair y(inv), minus_s(-scale), magic(12582912.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float m = fmaf(x[i], inv, 12582912.f);
-        b[i] = __float_as_uint(m);
-        off = fmaxf(off, fabsf(fmaf(x[i], inv, 12582912.f - m)));
+      for (int i = 0; i < 4; ++i) {
+        const Pair q0 = mul2(x[i], y);
+        const Pair q1 = fma2(fma2(q0, minus_s, x[i]), y, q0);
+        const Pair q2 = fma2(fma2(q1, minus_s, x[i]), y, q1);
+        const float2 m = add2(q2, magic).f();
+        b[2 * i] = __float_as_uint(m.x);
+        b[2 * i + 1] = __float_as_uint(m.y);
       }
-    }
-    if (off > 0.5f - 0x1p-14f) {
-#pragma unroll 1
-      for (int i = 0; i < 8; ++i) {
-        // (a rolled loop over registers: selects instead of indexing)
-        float v = x[0];
+    } else {
+      if (!some) return make_uint2(0u, 0u);
 #pragma unroll
-        for (int u = 1; u < 8; ++u) v = u == i ? x[u] : v;
-        const uint32_t c = code(v);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) b[u] = u == i ? c : b[u];
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = x[i].f();
+        b[2 * i] = (uint32_t)min(127, max(-127, __float2int_rn(__fdiv_rn(f.x, scale))));
+        b[2 * i + 1] = (uint32_t)min(127, max(-127, __float2int_rn(__fdiv_rn(f.y, scale))));
       }
     }
     return make_uint2(pack(b[0], b[1], b[2], b[3]), pack(b[4], b[5], b[6], b[7]));

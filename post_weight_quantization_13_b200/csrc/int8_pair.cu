@@ -291,8 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 16; ++i) y[i] += vbias[c + i];
           }
           alignas(16) T o[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = from_f32<T>(y[i]);
+          round_n<16>(y, o);
           // 16-byte unit u of row r sits at unit u ^ (r & 7): neither the row
           // owner's writes nor the row-wise reads below meet in a bank
 #pragma unroll

@@ -127,9 +127,9 @@ __device__ __forceinline__ void quantize_block(const RowsParams& kp, int4* codes
       if (t < kp.tokens) {
         const Raw8<X> r = load_columns((const X*)kp.x + t * kp.ldx,
                                        (s >> 1) * kSlice + 16 * (int)threadIdx.x + 8 * (s & 1), kp.in, kp.vec);
-        float f[8];
+        Pair f[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = r.get(i);
+        for (int i = 0; i < 4; ++i) f[i] = get2(r, i);
         c = scale.codes(f);
         total = __dp4a((int)c.x, 0x01010101, __dp4a((int)c.y, 0x01010101, total));
       }

@@ -43,6 +43,9 @@ def _untouched(buf, rows, cols, fill=7.0):
     (1, 1, F32, 0), (1, 4096, BF16, 0), (3, 7, F16, 0), (5, 512, F16, 0), (9, 513, BF16, 3), (2, 1000, F32, 1),
     (33, 4096, F16, 8), (4, 11008, F16, 0), (2, 16384, BF16, 0), (3, 16385, F32, 0), (2, 32768, F32, 0),
     (1001, 77, BF16, 0), (6, 32767, F16, 0),
+    # many rows: the streaming kernel, its ring going round, and what it leaves to the other
+    (3001, 1024, BF16, 8), (1500, 4096, F32, 4), (2000, 11008, F16, 0), (700, 32768, F32, 0), (900, 1032, F16, 1),
+    (40000, 512, BF16, 0),
 ])
 def test_quantize_tokens_is_the_definition(lib, tokens, d, dtype, pad):
     x = _values(_rng(1, tokens, d), tokens, d, dtype)
