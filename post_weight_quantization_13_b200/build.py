@@ -1,4 +1,6 @@
-"""Build libgptq.so in-tree for sm_100a with nvcc (no torch involved).
+"""Build libgptq.so in-tree for sm_100a with nvcc (no torch involved), and
+_serving.so, the CPython module behind serving.py's allocating calls, with g++
+against torch's headers.
 
     python post_weight_quantization_13_b200/build.py [--force]
 
@@ -6,7 +8,7 @@
 the library this script builds)
 
 Objects go to ``post_weight_quantization_13_b200/_build/``; the shared
-library lands next to this file.  Translation units compile in parallel and
+libraries land next to this file.  Translation units compile in parallel and
 are rebuilt only when a source or header is newer than the library.
 """
 from __future__ import annotations
@@ -23,6 +25,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgptq.so")
+EXT = os.path.join(HERE, "_serving.so")
+EXT_SOURCE = os.path.join(CSRC, "serving_ext.cpp")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -46,16 +50,49 @@ def _inputs():
         glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
+def _newer(target, inputs) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(p) <= os.path.getmtime(target) for p in inputs)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _inputs())
+    return _newer(LIB, _inputs())
+
+
+def ext_up_to_date() -> bool:
+    return _newer(EXT, [EXT_SOURCE, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def build_ext(verbose: bool = False) -> str:
+    import sysconfig
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = EXT + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"],
+           EXT_SOURCE, "-o", tmp, LIB, "-Wl,-rpath,$ORIGIN", "-L", os.path.join(base, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {EXT_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    if verbose:
+        sys.stderr.write(r.stderr)
+    os.replace(tmp, EXT)
+    return EXT
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
+    if force or not up_to_date():
+        _build_lib(verbose, ptxas_info)
+    if force or not ext_up_to_date():
+        build_ext(verbose)
+    return LIB
+
+
+def _build_lib(verbose: bool, ptxas_info: bool) -> None:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_info else []
@@ -73,12 +110,11 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     with ThreadPoolExecutor(max(1, min(8, os.cpu_count() or 1))) as ex:
         objs = list(ex.map(compile_one, sources()))
     tmp = LIB + ".tmp"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
+    cmd = [cc, *ARCH, "-shared", "-Xlinker", "-soname=libgptq.so", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

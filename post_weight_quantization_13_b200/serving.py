@@ -21,7 +21,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import _check, _i64, _p, _stream, lib
+from . import GptqError, _check, _i64, _p, _stream, lib
+from . import _serving  # type: ignore[attr-defined]  (built beside libgptq.so; there is no fallback)
 
 _NORMS = {"rms": 0, "layer": 1}
 _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
@@ -82,10 +83,13 @@ class Int8Tokens(NamedTuple):
     sum: torch.Tensor                     # int32 [tokens]
 
 
+_serving.init(GptqError, Int8Tokens)
+
+
 # ------------------------------------------------------------------ checks
 # The library sees addresses only: types, shapes and devices are checked here.
-# At decode these lines cost as much as the kernels they launch, so they touch
-# each tensor's attributes as few times as they can.
+# (The allocating calls below go through _serving.so, which makes the same
+# checks: at decode these lines cost more than the kernels they launch.)
 _CODES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -317,17 +321,9 @@ def int8_layer(r, bits: int) -> Int8Layer:
     return Int8Layer(weight, scales.reshape(-1), zero)
 
 
-def _new_tokens(T, d, dev):
-    return Int8Tokens(_int8_rows(T, d, dev), torch.empty(T, dtype=torch.float32, device=dev),
-                      torch.empty(T, dtype=torch.int32, device=dev))
-
-
 def quantize_tokens(X) -> Int8Tokens:
     """X [tokens, in] (f16, bf16 or f32) with a scale for each token."""
-    _ld(X, "X")
-    x = _new_tokens(*X.shape, X.device)
-    gptq_quantize_tokens(X, *x)
-    return x
+    return _serving.quantize(X)
 
 
 def norm_tokens(h, y=None, weight=None, *, bias=None, post_weight=None, post_bias=None, gate=None, alpha=1.0,
@@ -343,52 +339,25 @@ def norm_tokens(h, y=None, weight=None, *, bias=None, post_weight=None, post_bia
     Without y and with alpha 1, h' is h and h itself is returned."""
     if weight is None:
         raise ValueError("weight (the pre-norm's) is needed")
-    _ld(h, "h")
-    T, d = h.shape
-    dev = h.device
-    h_out = h if inplace else None if y is None and alpha == 1.0 else torch.empty((T, d), dtype=h.dtype, device=dev)
-    x, tokens = (None, _new_tokens(T, d, dev)) if quantize else \
-        (torch.empty((T, d), dtype=weight.dtype, device=dev), None)
-    gptq_norm_tokens(h, y, weight, bias, post_weight, post_bias, gate, alpha, beta, kind, eps, h_out, x, tokens)
-    return (h if h_out is None else h_out), (tokens if quantize else x)
-
-
-def _ws_for(x, device):
-    n = lib.gptq_linear_int8_ws_bytes(*x.shape)
-    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+    if kind not in _NORMS:
+        raise ValueError(f"kind must be one of {sorted(_NORMS)}, got {kind!r}")
+    return _serving.norm(h, y, weight, bias, post_weight, post_bias, gate, alpha, beta, _NORMS[kind], eps, quantize,
+                         inplace)
 
 
 def linear_int8(x, layer, bias=None, dtype=None):
     """x [tokens, in] times an Int8Layer (or (weight, scale[, zero])), plus
     bias (float32).  A floating x is quantized by token first; the result has
     ``dtype``, by default x's (bfloat16 for Int8Tokens)."""
-    out = layer[0].shape[0]
-    if isinstance(x, Int8Tokens):
-        q = x.q
-        Y = torch.empty((q.shape[0], out), dtype=dtype or torch.bfloat16, device=q.device)
-        gptq_matmul_int8(x, layer, Y, bias)
-    else:
-        _ld(x, "x")
-        dev = x.device
-        Y = torch.empty((x.shape[0], out), dtype=dtype or x.dtype, device=dev)
-        gptq_linear_int8(x, layer, Y, _ws_for(x, dev), bias)
-    return Y
+    return _serving.linear(x, layer, bias, dtype)
 
 
 def gated_int8(x, gate, up, act="silu", dtype=None):
     """act(x gate^T) * (x up^T) in one kernel; x, gate, up and dtype as in
     linear_int8, act one of "silu", "gelu", "gelu_tanh"."""
-    out = gate[0].shape[0]
-    if isinstance(x, Int8Tokens):
-        q = x.q
-        Y = torch.empty((q.shape[0], out), dtype=dtype or torch.bfloat16, device=q.device)
-        gptq_matmul_int8_gated(x, gate, up, Y, act)
-    else:
-        _ld(x, "x")
-        dev = x.device
-        Y = torch.empty((x.shape[0], out), dtype=dtype or x.dtype, device=dev)
-        gptq_linear_int8_gated(x, gate, up, Y, _ws_for(x, dev), act)
-    return Y
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    return _serving.gated(x, gate, up, _ACTS[act], dtype)
 
 
 def mlp_int8(h, y, weight, gate, up, down, act="silu", **norm):
