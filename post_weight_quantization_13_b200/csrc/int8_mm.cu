@@ -15,7 +15,7 @@
 // the result independent of the split, and no workspace or atomic is needed.
 //   warp 0     TMA producer (one thread)
 //   warp 1     tensor memory, tcgen05.mma.kind::i8 (one thread)
-//   warps 2-5  epilogue, or their partial sums into the shared memory of the
+//   warps 2-9  epilogue, or their partial sums into the shared memory of the
 //              rank that finishes the token, then that rank's epilogue
 // Every wait is bounded; a wait that gives up raises ST_TIMEOUT in the
 // library's int8 status word, and the CTA drains and leaves.
@@ -33,7 +33,8 @@
 namespace gptq {
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kEpilogue = 256;           // threads of the epilogue: two warps a tensor-memory quarter
+constexpr int kThreads = 64 + kEpilogue;
 constexpr int kBK = 128;                 // int8 elements of k per stage row (128-byte swizzle)
 constexpr int kTileM = 128;              // channels of a tile
 constexpr int kTileBytes = kTileM * kBK;
@@ -105,6 +106,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kt0 = (int)((int64_t)kp.ktiles * rank / split), kt1 = (int)((int64_t)kp.ktiles * (rank + 1) / split);
   const int ntile = kp.ntile;
 
+  const int ahead = min(kp.stages, kt1 - kt0);  // k-tiles that need not wait for a free stage
+  const uint32_t bytes = (uint32_t)(G * kTileBytes + ntile * kBK);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kp.stages; ++s) {
       mbar_init(&full[s], 1);
@@ -114,6 +117,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    // The weights do not come from the kernel before this one: the first
+    // stages' are on their way while the rest is set up and the tokens are
+    // quantized.
+    for (int i = 0; i < ahead; ++i) {
+      mbar_arrive_expect_tx(&full[i], bytes);
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        tma_load_2d(smem + (size_t)i * kp.stage_bytes + g * kTileBytes, &maps.w[g], &full[i], (kt0 + i) * kBK, n0);
+    }
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, (uint32_t)kp.tmem_cols);
@@ -130,16 +142,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       const int stages = kp.stages, stage_bytes = kp.stage_bytes;
-      const uint32_t bytes = (uint32_t)(G * kTileBytes + ntile * kBK);
-      // The weights do not come from the kernel before this one: the first
-      // stages' are on their way before it has finished with the tokens.
-      const int ahead = min(stages, kt1 - kt0);
-      for (int i = 0; i < ahead; ++i) {
-        uint8_t* sb = smem + (size_t)i * stage_bytes;
-        mbar_arrive_expect_tx(&full[i], bytes);
-#pragma unroll
-        for (int g = 0; g < G; ++g) tma_load_2d(sb + g * kTileBytes, &maps.w[g], &full[i], (kt0 + i) * kBK, n0);
-      }
       grid_dependency_wait();
       for (int i = 0; i < ahead; ++i)
         tma_load_2d(smem + (size_t)i * stage_bytes + G * kTileBytes, &maps.x, &full[i], (kt0 + i) * kBK, t0);
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (split > 1) cluster_wait();
   } else {
-    const int quarter = warp & 3, e = threadIdx.x - 64;
+    const int quarter = warp & 3, second = (warp - 2) / 4, e = threadIdx.x - 64;
     const int c = quarter * 32 + lane;
     const uint32_t tmem = tbase + ((uint32_t)(quarter * 32) << 16);
     // Everything the epilogue reads from memory is fetched under the main
@@ -219,25 +221,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       bias[i] = G == 1 && in && kp.bias ? __ldg(kp.bias + n + i) : 0.f;
     }
     grid_dependency_wait();
-    for (int j = e; j < ntile; j += 128) {
+    for (int j = e; j < ntile; j += kEpilogue) {
       const bool in = t0 + j < kp.tokens;
       tscale[j] = in ? kp.tscale[t0 + j] : 0.f;
       tsum[j] = in ? kp.tsum[t0 + j] : 0;
     }
-    named_bar_sync(1, 128);
+    named_bar_sync(1, kEpilogue);
     const int live = min(ntile, kp.tokens - t0);  // tokens of the tile inside the result
-    bool ok = mbar_wait_sleep(acc_full, 0);
-    if (!ok) {
+    if (!mbar_wait_sleep(acc_full, 0)) {
       raise_status(&g_int8_status, ST_TIMEOUT);
       *abort_flag = 1;
     }
     __syncwarp();
     tc_fence_after();
+    // sixteen tokens at a time, the quarter's two warps in turn
     if (split == 1) {
       // a token at a time, 32 neighbouring channels a warp
       T* const col = (T*)kp.Y + (int64_t)t0 * kp.ldy + n;
 #pragma unroll 1
-      for (int j0 = 0; j0 < live; j0 += 16) {
+      for (int j0 = 16 * second; j0 < live; j0 += 32) {
         float a[16], u[16];
         tmem_ld16(tmem + (uint32_t)j0, a);
         if (G == 2) tmem_ld16(tmem + (uint32_t)(ntile + j0), u);
@@ -258,16 +260,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       cluster_wait();
       const int share = ntile / split;
 #pragma unroll 1
-      for (int j0 = 0; j0 < ntile; j0 += 16) {
+      for (int j0 = 16 * second; j0 < ntile; j0 += 32) {
+        int owner = j0 / share, j = j0 - owner * share;
+        uint32_t at = map_to_rank(smem_u32(pushed + (rank * G * share) * kTileM + c), (uint32_t)owner);
+        float v[G][16];
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          float v[16];
-          tmem_ld16(tmem + (uint32_t)(g * ntile + j0), v);
+        for (int g = 0; g < G; ++g) tmem_ld16(tmem + (uint32_t)(g * ntile + j0), v[g]);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int owner = (j0 + i) / share, j = (j0 + i) % share;
-            st_cluster(map_to_rank(smem_u32(pushed + ((rank * G + g) * share + j) * kTileM + c), (uint32_t)owner),
-                       __float_as_int(v[i]));
+        for (int i = 0; i < 16; ++i) {
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+            st_cluster(at + (uint32_t)((g * share + j) * kTileM * 4), __float_as_int(v[g][i]));
+          if (++j == share) {
+            j = 0;
+            at = map_to_rank(smem_u32(pushed + (rank * G * share) * kTileM + c), (uint32_t)min(++owner, split - 1));
           }
         }
       }
@@ -276,19 +282,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       cluster_arrive();  // second phase: all partial sums are in place
       cluster_wait();
 #pragma unroll 1
-      for (int j = warp - 2; j < share; j += 4) {
+      for (int j = warp - 2; j < share; j += kEpilogue / 32) {
         const int at = rank * share + j;
         if (at >= live) break;
+        int4 part[G][kMaxSplit];
+#pragma unroll
+        for (int r = 0; r < kMaxSplit; ++r)
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+            part[g][r] = r < split ? *reinterpret_cast<const int4*>(pushed + ((r * G + g) * share + j) * kTileM + V * lane)
+                                   : make_int4(0, 0, 0, 0);
         int acc[G][V];
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          int4 sum = make_int4(0, 0, 0, 0);
-          for (int r = 0; r < split; ++r) {
-            const int4 b = *reinterpret_cast<const int4*>(pushed + ((r * G + g) * share + j) * kTileM + V * lane);
-            sum.x += b.x;
-            sum.y += b.y;
-            sum.z += b.z;
-            sum.w += b.w;
+          int4 sum = part[g][0];
+#pragma unroll
+          for (int r = 1; r < kMaxSplit; ++r) {
+            sum.x += part[g][r].x;
+            sum.y += part[g][r].y;
+            sum.z += part[g][r].z;
+            sum.w += part[g][r].w;
           }
           acc[g][0] = sum.x;
           acc[g][1] = sum.y;
@@ -342,6 +355,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tbase, (uint32_t)kp.tmem_cols);
   }
+}
+
+// ------------------------------------------------------------------- plan
+// Which kernel takes a product, and in which tiles.
+struct Plan {
+  bool pair;
+  int bn;            // pair kernel: channels of a tile
+  int ntile, split;  // split kernel: tokens of a tile, CTAs that share its k
+};
+
+Plan make_plan(int G, int64_t tokens, int64_t in, int64_t out, int sms) {
+  Plan p = {};
+  p.pair = tokens > 512;
+  p.bn = 256;
+  p.ntile = (int)std::min<int64_t>(G == 2 ? 64 : 128, (tokens + 15) / 16 * 16);
+  const int64_t ktiles = (in + kBK - 1) / kBK;
+  const int64_t tiles = ((out + kTileM - 1) / kTileM) * ((tokens + p.ntile - 1) / p.ntile);
+  p.split = 1;
+  while (p.split < kMaxSplit && tiles * p.split * 2 <= sms && ktiles >= p.split * 4) p.split *= 2;
+  return p;
 }
 
 // ------------------------------------------------------------------- host
@@ -406,17 +439,14 @@ cudaError_t launch_split(const SplitMaps& maps, const MmParams& kp, int64_t tile
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Tiles of 128 channels by up to 128 tokens; k is split over 2, 4 or 8 CTAs
-// while the tiles leave SMs idle and every CTA keeps at least two k-tiles.
 template <int G>
 cudaError_t run_split(MmParams kp, const gptq_int8_tokens_t* x, const gptq_int8_layer_t* const (&w)[2],
-                      gptq_dtype_t yt, bool follows, cudaStream_t st, int sms) {
-  kp.ntile = std::min(G == 2 ? 64 : 128, (kp.tokens + 15) / 16 * 16);
+                      gptq_dtype_t yt, const Plan& plan, bool follows, cudaStream_t st) {
+  kp.ntile = plan.ntile;
+  kp.split = plan.split;
   kp.ctiles = (kp.out + kTileM - 1) / kTileM;
   kp.ktiles = (kp.in + kBK - 1) / kBK;
   const int64_t tiles = (int64_t)kp.ctiles * ((kp.tokens + kp.ntile - 1) / kp.ntile);
-  kp.split = 1;
-  while (kp.split < kMaxSplit && tiles * kp.split * 2 <= sms && kp.ktiles >= kp.split * 4) kp.split *= 2;
   kp.stage_bytes = G * kTileBytes + kp.ntile * kBK;
   kp.push_bytes = kp.split > 1 ? G * kp.ntile * kTileM * 4 : 0;
   kp.tmem_cols = 32;
@@ -442,8 +472,8 @@ cudaError_t run_split(MmParams kp, const gptq_int8_tokens_t* x, const gptq_int8_
 
 template <int G>
 cudaError_t run(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const gptq_int8_layer_t* const (&w)[2],
-                int64_t out, const float* bias, int act, void* Y, gptq_dtype_t yt, int64_t ldy, bool follows,
-                cudaStream_t st) {
+                int64_t out, const float* bias, int act, void* Y, gptq_dtype_t yt, int64_t ldy, const Plan& plan,
+                bool follows, cudaStream_t st) {
   MmParams kp = {};
   kp.tscale = x->scale;
   kp.tsum = x->sum;
@@ -459,14 +489,11 @@ cudaError_t run(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const g
   kp.in = (int)in;
   kp.act = act;
   kp.vec = (uintptr_t)Y % 16 == 0 && (ldy * (yt == GPTQ_F32 ? 4 : 2)) % 16 == 0;
-  return run_split<G>(kp, x, w, yt, follows, st, device_info().sms);
+  return run_split<G>(kp, x, w, yt, plan, follows, st);
 }
 
 // Whether the rows kernel (int8_rows.cu) takes a product.
 bool few(int64_t tokens) { return tokens <= 2; }
-
-// Whether the pair kernel (int8_pair.cu) does.
-bool many(int64_t tokens) { return tokens > 512; }
 
 // follows: the kernel launched before on st is the quantizer that wrote x, and
 // this one may be set up while it runs.
@@ -474,14 +501,15 @@ cudaError_t multiply(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, co
                      int64_t out, const float* bias, int act, void* Y, gptq_dtype_t yt, int64_t ldy, bool follows,
                      cudaStream_t st) {
   if (few(tokens)) return rows_int8(nullptr, 0, 0, x, tokens, in, w, out, bias, act, Y, yt, ldy, st);
-  if (many(tokens)) {
+  const Plan plan = make_plan(w[1] ? 2 : 1, tokens, in, out, device_info().sms);
+  if (plan.pair) {
     uint32_t* status = nullptr;
     const cudaError_t e = int8_status_word(&status);
     if (e != cudaSuccess) return e;
-    return pair_int8(x, tokens, in, w, out, bias, act, Y, yt, ldy, follows, status, st);
+    return pair_int8(x, tokens, in, w, out, bias, act, Y, yt, ldy, plan.bn, follows, status, st);
   }
-  if (w[1]) return run<2>(x, tokens, in, w, out, bias, act, Y, yt, ldy, follows, st);
-  return run<1>(x, tokens, in, w, out, bias, act, Y, yt, ldy, follows, st);
+  if (w[1]) return run<2>(x, tokens, in, w, out, bias, act, Y, yt, ldy, plan, follows, st);
+  return run<1>(x, tokens, in, w, out, bias, act, Y, yt, ldy, plan, follows, st);
 }
 
 // The workspace of a product that quantizes its tokens: codes, scales, sums.

@@ -14,8 +14,12 @@
 //   warp 0     TMA producer: its own operand halves; the transactions of both
 //              CTAs are counted on the first CTA's barrier
 //   warp 1     (first CTA) issues the pair's MMAs and commits them to both
-//   warps 2-5  epilogue: scales, bias or activation, and 128-byte row pieces
-//              through shared memory to coalesced stores
+//   warps 2-9  epilogue: scales, bias or activation, and 64-byte row pieces
+//              through shared memory to coalesced stores.  Two warps share a
+//              quarter of tensor memory and halve its columns between them:
+//              the last tile's epilogue has nothing to hide under, and with
+//              four warps it took 4.9 of the 19 us of a product of one tile
+//              (256 x 256, k 4096).
 // Two 256-column accumulators in tensor memory let a tile's epilogue run
 // under the next tile's main loop.  Every wait is bounded (see split kernel).
 #include <algorithm>
@@ -28,10 +32,11 @@
 namespace gptq {
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kEpilogue = 256;               // threads of the epilogue: two warps a tensor-memory quarter
+constexpr int kThreads = 64 + kEpilogue;
 constexpr int kBK = 128;                     // bytes of k per stage
 constexpr int kATile = 128 * kBK;            // a CTA's tokens of one stage
-constexpr int kStageOut = 4 * 32 * 128;      // epilogue staging: 32 rows x 128 bytes a warp
+constexpr int kStageOut = 8 * 32 * 64;       // epilogue staging: 32 rows x 64 bytes a warp
 constexpr int kVectors = 256 * 3 * 4;        // a tile's scales, zeros, bias
 constexpr int kGroup = 8;                    // token tiles that walk the channels together
 
@@ -92,17 +97,28 @@ __device__ __forceinline__ void tile_at(const PairParams& kp, int tile, int* mt,
   *nt = rest / rows;
 }
 
-// Sixteen columns of sums (32-bit integers in v) to the product's values.
-__device__ __forceinline__ void scale_columns(const float (&v)[16], float (&y)[16], const float* scale,
-                                              const int* zero, int sum, float ts) {
+// Byte offset of 16-byte unit u (0..3) of row r of a 64-byte-wide staging tile.
+__device__ __forceinline__ uint32_t sw64(int r, int u) { return (uint32_t)(r * 64 + ((u ^ (r >> 1 & 3)) << 4)); }
+
+// N columns of sums (32-bit integers in v) to the product's values; zeros:
+// some channel has one.
+template <int N>
+__device__ __forceinline__ void scale_columns(const float (&v)[N], Pair (&y)[N / 2], const float* scale,
+                                              const int* zero, bool zeros, int sum, float ts) {
+  const Pair t(ts);
 #pragma unroll
-  for (int i = 0; i < 16; i += 4) {
+  for (int i = 0; i < N; i += 4) {
+    int a[4] = {__float_as_int(v[i]), __float_as_int(v[i + 1]), __float_as_int(v[i + 2]), __float_as_int(v[i + 3])};
+    if (zeros) {
+      const int4 z = *reinterpret_cast<const int4*>(zero + i);
+      a[0] -= z.x * sum;
+      a[1] -= z.y * sum;
+      a[2] -= z.z * sum;
+      a[3] -= z.w * sum;
+    }
     const float4 s = *reinterpret_cast<const float4*>(scale + i);
-    const int4 z = *reinterpret_cast<const int4*>(zero + i);
-    y[i + 0] = scaled(__float_as_int(v[i + 0]), z.x, sum, ts, s.x);
-    y[i + 1] = scaled(__float_as_int(v[i + 1]), z.y, sum, ts, s.y);
-    y[i + 2] = scaled(__float_as_int(v[i + 2]), z.z, sum, ts, s.z);
-    y[i + 3] = scaled(__float_as_int(v[i + 3]), z.w, sum, ts, s.w);
+    y[i / 2] = mul2(mul2(Pair((float)a[0], (float)a[1]), t), Pair(s.x, s.y));
+    y[i / 2 + 1] = mul2(mul2(Pair((float)a[2], (float)a[3]), t), Pair(s.z, s.w));
   }
 }
 
@@ -126,6 +142,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int rank = (int)cluster_rank();
   const int half = kp.bn / 2;  // channels a CTA loads
 
+  if (threadIdx.x == 64) {
+    tma_prefetch_desc(&maps.x);
+    tma_prefetch_desc(&maps.w[G == 2 ? rank : 0]);
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kp.stages; ++s) {
       mbar_init(&full[s], 1);
@@ -133,7 +153,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 8);  // four epilogue warps of each CTA
+      mbar_init(&acc_empty[b], 2 * kEpilogue / 32);  // the epilogue warps of both CTAs
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -225,13 +245,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    constexpr int CW = 128 / (int)sizeof(T);  // columns of a 128-byte row piece
+    constexpr int CW = 64 / (int)sizeof(T);  // columns of a 64-byte row piece
+    constexpr int STEP = CW < 16 ? CW : 16;  // columns of a step, see below
     const int quarter = warp & 3, e = threadIdx.x - 64;
     const int bn = kp.bn, width = G == 2 ? half : bn;  // channels of the tile's output
-    uint8_t* mine = staging + (warp - 2) * (32 * 128);
+    const int c_begin = (warp - 2) / 4 * (width / 2), c_end = c_begin + width / 2;  // this warp's
+    uint8_t* mine = staging + (warp - 2) * (32 * 64);
     float* const vscale = vectors;                 // [bn]: gated, gate then up
     int* const vzero = (int*)(vectors + 256);      // [bn]
     float* const vbias = vectors + 512;            // [bn]
+    const bool zeros = kp.wzero[0] || (G == 2 && kp.wzero[1]), biased = G == 1 && kp.bias;
     int step = 0;
     for (int tile = pair; tile < kp.tiles; tile += kp.pairs, ++step) {
       int mt, nt;
@@ -239,66 +262,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int n0 = nt * width;
       const int t = mt * 256 + rank * 128 + quarter * 32 + lane;
       // the tile's vectors, while its main loop runs
-      named_bar_sync(1, 128);  // the previous tile's are no longer read
-      for (int i = e; i < bn; i += 128) {
+      named_bar_sync(1, kEpilogue);  // the previous tile's are no longer read
+      for (int i = e; i < bn; i += kEpilogue) {
         const int g = G == 2 ? i / half : 0, n = n0 + (G == 2 ? i % half : i);
         const bool in = n < kp.out;
         vscale[i] = in ? __ldg(kp.wscale[g] + n) : 0.f;
         vzero[i] = in && kp.wzero[g] ? __ldg(kp.wzero[g] + n) : 0;
-        vbias[i] = G == 1 && in && kp.bias ? __ldg(kp.bias + n) : 0.f;
+        vbias[i] = in && biased ? __ldg(kp.bias + n) : 0.f;
       }
       const float ts = t < kp.tokens ? __ldg(kp.tscale + t) : 0.f;
       const int sum = t < kp.tokens ? __ldg(kp.tsum + t) : 0;
-      named_bar_sync(1, 128);
+      named_bar_sync(1, kEpilogue);
       const int buf = step & 1, use = step >> 1;
       if (!mbar_wait_sleep(&acc_full[buf], use & 1)) {
         raise_status(kp.status, ST_TIMEOUT);
         *abort_flag = 1;
       }
       if (*abort_flag) *epilogue_abort = 1;
-      // all four warps leave together: they share barrier 1
-      named_bar_sync(1, 128);
+      // all warps leave together: they share barrier 1
+      named_bar_sync(1, kEpilogue);
       if (*epilogue_abort) break;
       tc_fence_after();
       const uint32_t tmem = tbase + (uint32_t)buf * 256u + ((uint32_t)(quarter * 32) << 16);
       T* const rows = (T*)kp.Y + (int64_t)(t - lane) * kp.ldy;
       const int live = min(32, kp.tokens - (t - lane));  // rows of this warp inside the result
-      for (int c0 = 0; c0 < width; c0 += CW) {
+      for (int c0 = c_begin; c0 < c_end; c0 += CW) {
         // sixteen columns a step, not unrolled further: the loop has to stay
         // in the instruction cache (unrolled over 64 columns, the gated form
-        // waited for instructions most of the time and took 1.6 times as long)
+        // waited for instructions most of the time and took 1.4 times as long)
 #pragma unroll 1
-        for (int p = 0; p < CW / 16; ++p) {
-          const int c = c0 + 16 * p;
-          float a[16], y[16];
+        for (int p = 0; p < CW / STEP; ++p) {
+          const int c = c0 + STEP * p;
+          float a[STEP];
+          Pair y[STEP / 2];
           tmem_ld16(tmem + (uint32_t)c, a);
-          scale_columns(a, y, vscale + c, vzero + c, sum, ts);
+          scale_columns<STEP>(a, y, vscale + c, vzero + c, zeros, sum, ts);
           if (G == 2) {
+            float b[STEP];
+            Pair u[STEP / 2];
+            tmem_ld16(tmem + (uint32_t)(half + c), b);
+            scale_columns<STEP>(b, u, vscale + half + c, vzero + half + c, zeros, sum, ts);
             if (kp.act == GPTQ_ACT_GELU) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) y[i] = activate(y[i], GPTQ_ACT_GELU);
+              for (int i = 0; i < STEP / 2; ++i) {
+                const float2 f = y[i].f();
+                y[i] = mul2(Pair(activate(f.x, GPTQ_ACT_GELU), activate(f.y, GPTQ_ACT_GELU)), u[i]);
+              }
             } else {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) y[i] = activate(y[i], kp.act);
+              for (int i = 0; i < STEP / 2; ++i) {
+                const float2 f = y[i].f();
+                y[i] = mul2(Pair(activate(f.x, kp.act), activate(f.y, kp.act)), u[i]);
+              }
             }
-            float u[16];
-            tmem_ld16(tmem + (uint32_t)(half + c), a);
-            scale_columns(a, u, vscale + half + c, vzero + half + c, sum, ts);
+          } else if (biased) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] *= u[i];
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] += vbias[c + i];
+            for (int i = 0; i < STEP; i += 4) {
+              const float4 b = *reinterpret_cast<const float4*>(vbias + c + i);
+              y[i / 2] = add2(y[i / 2], Pair(b.x, b.y));
+              y[i / 2 + 1] = add2(y[i / 2 + 1], Pair(b.z, b.w));
+            }
           }
-          alignas(16) T o[16];
-          round_n<16>(y, o);
-          // 16-byte unit u of row r sits at unit u ^ (r & 7): neither the row
-          // owner's writes nor the row-wise reads below meet in a bank
+          alignas(16) T o[STEP];
 #pragma unroll
-          for (int u = 0; u < (int)sizeof(T); ++u)
-            *reinterpret_cast<uint4*>(mine + sw128(lane, p * (int)sizeof(T) + u)) = reinterpret_cast<const uint4*>(o)[u];
+          for (int i = 0; i < STEP / 2; ++i) {
+            const float2 f = y[i].f();
+            const float v[2] = {f.x, f.y};
+            round_n<2>(v, o + 2 * i);
+          }
+          // 16-byte unit u of row r sits at unit u ^ (r / 2 & 3): neither the
+          // row owner's writes nor the row-wise reads below meet in a bank
+#pragma unroll
+          for (int u = 0; u < STEP * (int)sizeof(T) / 16; ++u)
+            *reinterpret_cast<uint4*>(mine + sw64(lane, p * (STEP * (int)sizeof(T) / 16) + u)) =
+                reinterpret_cast<const uint4*>(o)[u];
         }
-        if (c0 + CW >= width) {
+        if (c0 + CW >= c_end) {
           // the accumulator is read: the next tile but one may have it
           tc_fence_before();
           __syncwarp();
@@ -307,19 +346,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (kp.vec && n0 + c0 + CW <= kp.out) {
 #pragma unroll
-          for (int r0 = 0; r0 < 32; r0 += 4) {
-            const int r = r0 + (lane >> 3);
+          for (int r0 = 0; r0 < 32; r0 += 8) {
+            const int r = r0 + (lane >> 2);
             if (r < live)
-              *reinterpret_cast<uint4*>((uint8_t*)(rows + r * kp.ldy + n0 + c0) + 16 * (lane & 7)) =
-                  *reinterpret_cast<const uint4*>(mine + sw128(r, lane & 7));
+              *reinterpret_cast<uint4*>((uint8_t*)(rows + r * kp.ldy + n0 + c0) + 16 * (lane & 3)) =
+                  *reinterpret_cast<const uint4*>(mine + sw64(r, lane & 3));
           }
         } else {
-          const int cols = min(CW, kp.out - n0 - c0);
-          for (int r = 0; r < live; ++r)
-            for (int c = lane; c < cols; c += 32) {
-              const int byte = c * (int)sizeof(T);
-              rows[r * kp.ldy + n0 + c0 + c] = *reinterpret_cast<const T*>(mine + sw128(r, byte >> 4) + (byte & 15));
-            }
+          const int c = lane % CW, cols = min(CW, kp.out - n0 - c0);
+          const int byte = c * (int)sizeof(T);
+          if (c < cols)
+            for (int r = lane / CW; r < live; r += 32 / CW)
+              rows[r * kp.ldy + n0 + c0 + c] = *reinterpret_cast<const T*>(mine + sw64(r, byte >> 4) + (byte & 15));
         }
         __syncwarp();
       }
@@ -371,8 +409,8 @@ cudaError_t launch(const PairMaps& maps, const PairParams& kp, bool follows, cud
 }  // namespace
 
 cudaError_t pair_int8(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const gptq_int8_layer_t* const (&w)[2],
-                      int64_t out, const float* bias, int act, void* Y, gptq_dtype_t yt, int64_t ldy, bool follows,
-                      uint32_t* status, cudaStream_t st) {
+                      int64_t out, const float* bias, int act, void* Y, gptq_dtype_t yt, int64_t ldy, int bn,
+                      bool follows, uint32_t* status, cudaStream_t st) {
   const int G = w[1] ? 2 : 1;
   PairParams kp = {};
   kp.tscale = x->scale;
@@ -390,7 +428,7 @@ cudaError_t pair_int8(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, c
   kp.vec = (uintptr_t)Y % 16 == 0 && (ldy * (yt == GPTQ_F32 ? 4 : 2)) % 16 == 0;
   kp.status = status;
   kp.ktiles = (int)((in + kBK - 1) / kBK);
-  kp.bn = 256;
+  kp.bn = bn;
   kp.stage_bytes = kATile + kp.bn / 2 * kBK;
   kp.stages = std::min(12, (232448 - 1024 - kStageOut - kVectors - 256) / kp.stage_bytes);
   kp.mtiles = (int)((tokens + 255) / 256);

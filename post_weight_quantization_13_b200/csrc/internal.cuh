@@ -97,10 +97,10 @@ cudaError_t rows_int8(const void* x, int xt, int64_t ldx, const gptq_int8_tokens
                       gptq_dtype_t yt, int64_t ldy, cudaStream_t st);
 // Both for many tokens (int8_pair.cu); a wait that gives up raises ST_TIMEOUT
 // in *status.  follows: launched behind the quantizer that wrote x, and may
-// be set up while it runs.
+// be set up while it runs.  bn: the pair's channels, 128 or 256.
 cudaError_t pair_int8(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const gptq_int8_layer_t* const (&w)[2],
-                      int64_t out, const float* bias, int act, void* Y, gptq_dtype_t yt, int64_t ldy, bool follows,
-                      uint32_t* status, cudaStream_t st);
+                      int64_t out, const float* bias, int act, void* Y, gptq_dtype_t yt, int64_t ldy, int bn,
+                      bool follows, uint32_t* status, cudaStream_t st);
 // A tensor map over a K-major int8 operand (rows x in, row stride ld bytes) in
 // boxes of box_rows rows by 128 bytes; what lies past the matrix reads as zero.
 bool int8_map(CUtensorMap* m, const int8_t* base, int64_t rows, int64_t in, int64_t ld, int box_rows);
