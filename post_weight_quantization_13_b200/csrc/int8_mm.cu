@@ -65,16 +65,6 @@ struct SplitMaps {
 };
 
 // ----------------------------------------------------------------- pieces
-// D[tmem] (+)= A[smem] B[smem]^T, signed 8-bit inputs, 32-bit integers.
-__device__ __forceinline__ void umma_i8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 __device__ __forceinline__ void st_cluster(uint32_t addr, int v) {
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -139,27 +129,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   // memory can be written to
   if (split > 1) cluster_arrive();
 
+  const uint32_t stage0 = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
   if (warp == 0) {
     if (lane == 0) {
       const int stages = kp.stages, stage_bytes = kp.stage_bytes;
       grid_dependency_wait();
       for (int i = 0; i < ahead; ++i)
-        tma_load_2d(smem + (size_t)i * stage_bytes + G * kTileBytes, &maps.x, &full[i], (kt0 + i) * kBK, t0);
+        tma_load_at(stage0 + i * stage_bytes + G * kTileBytes, &maps.x, full0 + 8 * i, (kt0 + i) * kBK, t0);
       int stage = 0;
-      uint32_t phase = 0;
-      for (int kt = kt0 + ahead; kt < kt1; ++kt) {
-        if (!mbar_wait(&empty[stage], phase)) {
+      uint32_t phase = 0, at = stage0;
+      for (int x = (kt0 + ahead) * kBK; x < kt1 * kBK; x += kBK) {
+        if (!wait_at(empty0 + 8 * stage, phase)) {
           raise_status(&g_int8_status, ST_TIMEOUT);
           *abort_flag = 1;
+          break;
         }
-        if (*abort_flag) break;
-        uint8_t* sb = smem + (size_t)stage * stage_bytes;
-        mbar_arrive_expect_tx(&full[stage], bytes);
+        expect_at(full0 + 8 * stage, bytes);
 #pragma unroll
-        for (int g = 0; g < G; ++g) tma_load_2d(sb + g * kTileBytes, &maps.w[g], &full[stage], kt * kBK, n0);
-        tma_load_2d(sb + G * kTileBytes, &maps.x, &full[stage], kt * kBK, t0);
+        for (int g = 0; g < G; ++g) tma_load_at(at + g * kTileBytes, &maps.w[g], full0 + 8 * stage, x, n0);
+        tma_load_at(at + G * kTileBytes, &maps.x, full0 + 8 * stage, x, t0);
+        at += stage_bytes;
         if (++stage == stages) {
           stage = 0;
+          at = stage0;
           phase ^= 1;
         }
       }
@@ -168,34 +160,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (split > 1) cluster_wait();
   } else if (warp == 1) {
     if (lane == 0) {
-      const int stages = kp.stages, stage_bytes = kp.stage_bytes;
+      const int stages = kp.stages;
       const uint32_t idesc = idesc_i8(kTileM, (uint32_t)ntile);
+      const uint32_t a0 = desc_low(stage0), b0 = desc_low(stage0 + G * kTileBytes);
+      const uint32_t desc_step = (uint32_t)kp.stage_bytes >> 4;
       int stage = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, at = 0;
       bool ok = true;
       for (int kt = kt0; kt < kt1; ++kt) {
-        if (!mbar_wait(&full[stage], phase)) {
+        if (!wait_at(full0 + 8 * stage, phase)) {
           raise_status(&g_int8_status, ST_TIMEOUT);
           *abort_flag = 1;
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t sb = smem_u32(smem + (size_t)stage * stage_bytes);
-        const uint32_t xb = sb + G * kTileBytes;
 #pragma unroll
         for (int kk = 0; kk < kBK / 32; ++kk)
 #pragma unroll
           for (int g = 0; g < G; ++g)
-            umma_i8(tbase + (uint32_t)(g * ntile), smem_desc_k_sw128(sb + g * kTileBytes + kk * 32),
-                    smem_desc_k_sw128(xb + kk * 32), idesc, (kt > kt0 || kk > 0) ? 1u : 0u);
-        umma_commit(&empty[stage]);
+            umma_i8<1>(tbase + (uint32_t)(g * ntile), a0 + at + g * (kTileBytes >> 4) + 2 * kk, b0 + at + 2 * kk, idesc,
+                       kk > 0 ? 1u : (uint32_t)(kt > kt0));
+        commit_at(empty0 + 8 * stage);
+        at += desc_step;
         if (++stage == stages) {
           stage = 0;
+          at = 0;
           phase ^= 1;
         }
       }
-      if (ok) umma_commit(acc_full);
+      if (ok) commit_at(smem_u32(acc_full));
     }
     __syncwarp();
     if (split > 1) cluster_wait();

@@ -59,33 +59,20 @@ struct PairMaps {
   CUtensorMap w[2];
 };
 
-__device__ __forceinline__ void umma_i8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Arrive on both CTAs' barrier at this offset once this thread's MMAs are done.
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"((uint16_t)3)
-      : "memory");
-}
 // A tile into this CTA's shared memory, counted on a barrier of the pair
 // given by its cluster address.
-__device__ __forceinline__ void load_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+__device__ __forceinline__ void load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
   asm volatile(
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
       "l"(map), "r"(bar), "r"(x), "r"(y)
       : "memory");
 }
+// Arrive on a barrier of the pair.  What it orders are reads of tensor memory,
+// complete behind tcgen05.wait and fenced: the release is block-wide, for a
+// cluster-wide one would wait for the epilogue's global stores.
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // The tile's first token and first channel.  kGroup token tiles walk the
@@ -175,31 +162,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int pair = (int)blockIdx.x / 2;
   grid_dependency_wait();  // what came before ran beside the set-up above
 
+  const uint32_t stage0 = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
   if (warp == 0) {
     if (lane == 0) {
       const int stages = kp.stages, stage_bytes = kp.stage_bytes, ktiles = kp.ktiles;
       const uint32_t bytes = 2u * (uint32_t)(kATile + half * kBK);  // of both CTAs
+      const uint32_t pair_full0 = map_to_rank(full0, 0);
       const CUtensorMap* wmap = &maps.w[G == 2 ? rank : 0];
       int stage = 0;
-      uint32_t phase = 0;
-      for (int tile = pair; tile < kp.tiles && !*abort_flag; tile += kp.pairs) {
+      uint32_t phase = 1, at = stage0;
+      bool ok = true;
+      for (int tile = pair; tile < kp.tiles && ok; tile += kp.pairs) {
         int mt, nt;
         tile_at(kp, tile, &mt, &nt);
         const int t0 = mt * 256 + rank * 128;
         const int n0 = G == 2 ? nt * half : nt * kp.bn + rank * half;
-        for (int kt = 0; kt < ktiles; ++kt) {
-          if (!mbar_wait(&empty[stage], phase ^ 1)) {
+        for (int x = 0; x < ktiles * kBK; x += kBK) {
+          if (!wait_at(empty0 + 8 * stage, phase)) {
             raise_status(kp.status, ST_TIMEOUT);
             *abort_flag = 1;
+            ok = false;
+            break;
           }
-          if (*abort_flag) break;
-          uint8_t* sb = smem + (size_t)stage * stage_bytes;
-          const uint32_t bar = map_to_rank(smem_u32(&full[stage]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], bytes);
-          load_pair(sb, &maps.x, bar, kt * kBK, t0);
-          load_pair(sb + kATile, wmap, bar, kt * kBK, n0);
+          if (rank == 0) expect_at(full0 + 8 * stage, bytes);
+          load_pair(at, &maps.x, pair_full0 + 8 * stage, x, t0);
+          load_pair(at + kATile, wmap, pair_full0 + 8 * stage, x, n0);
+          at += stage_bytes;
           if (++stage == stages) {
             stage = 0;
+            at = stage0;
             phase ^= 1;
           }
         }
@@ -207,12 +198,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      const int stages = kp.stages, stage_bytes = kp.stage_bytes, ktiles = kp.ktiles;
+      const int stages = kp.stages, ktiles = kp.ktiles;
       const uint32_t idesc = idesc_i8(256, (uint32_t)kp.bn);
+      const uint32_t a0 = desc_low(stage0), b0 = desc_low(stage0 + kATile), desc_step = (uint32_t)kp.stage_bytes >> 4;
       int stage = 0, step = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, at = 0;
       bool ok = true;
-      for (int tile = pair; tile < kp.tiles && ok && !*abort_flag; tile += kp.pairs, ++step) {
+      for (int tile = pair; tile < kp.tiles && ok; tile += kp.pairs, ++step) {
         const int buf = step & 1, use = step >> 1;
         if (use > 0 && !mbar_wait(&acc_empty[buf], (use - 1) & 1)) {
           raise_status(kp.status, ST_TIMEOUT);
@@ -222,25 +214,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t d = tbase + (uint32_t)buf * 256u;
         for (int kt = 0; kt < ktiles; ++kt) {
-          if (!mbar_wait(&full[stage], phase)) {
+          if (!wait_at(full0 + 8 * stage, phase)) {
             raise_status(kp.status, ST_TIMEOUT);
             *abort_flag = 1;
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sb = smem_u32(smem + (size_t)stage * stage_bytes);
+          umma_i8<2>(d, a0 + at, b0 + at, idesc, kt > 0);
 #pragma unroll
-          for (int kk = 0; kk < kBK / 32; ++kk)
-            umma_i8_pair(d, smem_desc_k_sw128(sb + kk * 32), smem_desc_k_sw128(sb + kATile + kk * 32), idesc,
-                         (kt > 0 || kk > 0) ? 1u : 0u);
-          commit_pair(&empty[stage]);
+          for (int kk = 1; kk < kBK / 32; ++kk) umma_i8<2>(d, a0 + at + 2 * kk, b0 + at + 2 * kk, idesc, 1u);
+          commit_pair_at(empty0 + 8 * stage);
+          at += desc_step;
           if (++stage == stages) {
             stage = 0;
+            at = 0;
             phase ^= 1;
           }
         }
-        if (ok) commit_pair(&acc_full[buf]);
+        if (ok) commit_pair_at(smem_u32(&acc_full[buf]));
       }
     }
   } else {
@@ -367,7 +359,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncwarp();
   if (*abort_flag && threadIdx.x == 32 && rank == 0) {
     // let the MMAs already issued finish before the memory goes away
-    commit_pair(drain);
+    commit_pair_at(smem_u32(drain));
     mbar_wait(drain, 0);
   }
   if (*abort_flag && threadIdx.x == 0) {  // and the copies
