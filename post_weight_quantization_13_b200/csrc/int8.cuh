@@ -153,13 +153,23 @@ __host__ __device__ constexpr uint32_t idesc_i8(uint32_t M, uint32_t N) {
   return (2u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
-// The loops that feed the tensor cores are single threads, whose every
-// instruction costs its latency: a k-tile of 128 bytes has to be issued in
-// less than the 512 cycles its largest MMAs take (and, with few tokens, in
-// the 200 its bytes take).  So they work on 32-bit shared-memory addresses,
-// step them by addition, and keep the constant half of a descriptor apart
-// (from generic pointers, with descriptors built for each MMA, a k-tile cost
-// 600 cycles whatever its size).
+// The loops that feed the tensor cores are run by whole warps, so that their
+// addresses and descriptors are uniform values; each copy, MMA or arrival is
+// done by one lane (`leader`, from elect_lane) under a predicate.  Run by a
+// single thread, every tcgen05.mma first moved its operands to uniform
+// registers: 58 cycles each, so that a k-tile of 128 bytes took 520 to 600
+// cycles to issue where its MMAs take 512 at most.  Addresses are 32-bit and
+// stepped by addition; the constant half of a descriptor is kept apart.
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t leader;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(leader));
+  return leader;
+}
 __device__ __forceinline__ bool wait_at(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -183,14 +193,20 @@ __device__ __forceinline__ bool wait_at(uint32_t bar, uint32_t parity) {
   }
   return false;
 }
-__device__ __forceinline__ void expect_at(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void tma_load_at(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+__device__ __forceinline__ void expect_at(uint32_t leader, uint32_t bar, uint32_t bytes) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-      "l"(map), "r"(bar), "r"(x), "r"(y)
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+      "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_at(uint32_t leader, uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
+                                            int y) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "@p cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(y), "r"(leader)
       : "memory");
 }
 // K-major operand with 128-byte swizzling (see smem_desc_k_sw128): the low
@@ -201,33 +217,39 @@ __device__ __forceinline__ uint32_t desc_low(uint32_t smem_addr) { return ((smem
 // D[tmem] (+)= A[smem] B[smem]^T, signed 8-bit inputs, 32-bit integers;
 // kGroup CTAs (cta_group).
 template <int kGroup>
-__device__ __forceinline__ void umma_i8(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc,
+__device__ __forceinline__ void umma_i8(uint32_t leader, uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc,
                                         uint32_t accumulate) {
   if constexpr (kGroup == 1)
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
         "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
-        "tcgen05.mma.cta_group::1.kind::i8 [%0], a, b, %4, p;\n\t}" ::"r"(d),
-        "r"(a_low), "r"(b_low), "r"(kDescHigh), "r"(idesc), "r"(accumulate)
+        "@q tcgen05.mma.cta_group::1.kind::i8 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+        "r"(a_low), "r"(b_low), "r"(kDescHigh), "r"(idesc), "r"(accumulate), "r"(leader)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
         "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
-        "tcgen05.mma.cta_group::2.kind::i8 [%0], a, b, %4, p;\n\t}" ::"r"(d),
-        "r"(a_low), "r"(b_low), "r"(kDescHigh), "r"(idesc), "r"(accumulate)
+        "@q tcgen05.mma.cta_group::2.kind::i8 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+        "r"(a_low), "r"(b_low), "r"(kDescHigh), "r"(idesc), "r"(accumulate), "r"(leader)
         : "memory");
 }
-__device__ __forceinline__ void commit_at(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void commit_at(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(leader)
+      : "memory");
 }
 // Arrive on both CTAs' barrier at this offset once this thread's MMAs are done.
-__device__ __forceinline__ void commit_pair_at(uint32_t bar) {
+__device__ __forceinline__ void commit_pair_at(uint32_t leader, uint32_t bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"((uint16_t)3)
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+      "@p tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::
+          "r"(bar),
+      "h"((uint16_t)3), "r"(leader)
       : "memory");
 }
 

@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = (uint32_t*)(drain + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = uniform_warp();
   const int lane = threadIdx.x & 31;
   const int split = kp.split;
   const int rank = split > 1 ? (int)cluster_rank() : 0;
@@ -131,66 +131,64 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const uint32_t stage0 = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
   if (warp == 0) {
-    if (lane == 0) {
-      const int stages = kp.stages, stage_bytes = kp.stage_bytes;
-      grid_dependency_wait();
-      for (int i = 0; i < ahead; ++i)
-        tma_load_at(stage0 + i * stage_bytes + G * kTileBytes, &maps.x, full0 + 8 * i, (kt0 + i) * kBK, t0);
-      int stage = 0;
-      uint32_t phase = 0, at = stage0;
-      for (int x = (kt0 + ahead) * kBK; x < kt1 * kBK; x += kBK) {
-        if (!wait_at(empty0 + 8 * stage, phase)) {
-          raise_status(&g_int8_status, ST_TIMEOUT);
-          *abort_flag = 1;
-          break;
-        }
-        expect_at(full0 + 8 * stage, bytes);
+    const uint32_t leader = elect_lane();
+    const int stages = kp.stages, stage_bytes = kp.stage_bytes;
+    grid_dependency_wait();
+    for (int i = 0; i < ahead; ++i)
+      tma_load_at(leader, stage0 + i * stage_bytes + G * kTileBytes, &maps.x, full0 + 8 * i, (kt0 + i) * kBK, t0);
+    int stage = 0;
+    uint32_t phase = 0, at = stage0;
+    for (int x = (kt0 + ahead) * kBK; x < kt1 * kBK; x += kBK) {
+      if (!wait_at(empty0 + 8 * stage, phase)) {
+        raise_status(&g_int8_status, ST_TIMEOUT);
+        *abort_flag = 1;
+        break;
+      }
+      expect_at(leader, full0 + 8 * stage, bytes);
 #pragma unroll
-        for (int g = 0; g < G; ++g) tma_load_at(at + g * kTileBytes, &maps.w[g], full0 + 8 * stage, x, n0);
-        tma_load_at(at + G * kTileBytes, &maps.x, full0 + 8 * stage, x, t0);
-        at += stage_bytes;
-        if (++stage == stages) {
-          stage = 0;
-          at = stage0;
-          phase ^= 1;
-        }
+      for (int g = 0; g < G; ++g) tma_load_at(leader, at + g * kTileBytes, &maps.w[g], full0 + 8 * stage, x, n0);
+      tma_load_at(leader, at + G * kTileBytes, &maps.x, full0 + 8 * stage, x, t0);
+      at += stage_bytes;
+      if (++stage == stages) {
+        stage = 0;
+        at = stage0;
+        phase ^= 1;
       }
     }
     __syncwarp();
     if (split > 1) cluster_wait();
   } else if (warp == 1) {
-    if (lane == 0) {
-      const int stages = kp.stages;
-      const uint32_t idesc = idesc_i8(kTileM, (uint32_t)ntile);
-      const uint32_t a0 = desc_low(stage0), b0 = desc_low(stage0 + G * kTileBytes);
-      const uint32_t desc_step = (uint32_t)kp.stage_bytes >> 4;
-      int stage = 0;
-      uint32_t phase = 0, at = 0;
-      bool ok = true;
-      for (int kt = kt0; kt < kt1; ++kt) {
-        if (!wait_at(full0 + 8 * stage, phase)) {
-          raise_status(&g_int8_status, ST_TIMEOUT);
-          *abort_flag = 1;
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < kBK / 32; ++kk)
-#pragma unroll
-          for (int g = 0; g < G; ++g)
-            umma_i8<1>(tbase + (uint32_t)(g * ntile), a0 + at + g * (kTileBytes >> 4) + 2 * kk, b0 + at + 2 * kk, idesc,
-                       kk > 0 ? 1u : (uint32_t)(kt > kt0));
-        commit_at(empty0 + 8 * stage);
-        at += desc_step;
-        if (++stage == stages) {
-          stage = 0;
-          at = 0;
-          phase ^= 1;
-        }
+    const uint32_t leader = elect_lane();
+    const int stages = kp.stages;
+    const uint32_t idesc = idesc_i8(kTileM, (uint32_t)ntile);
+    const uint32_t a0 = desc_low(stage0), b0 = desc_low(stage0 + G * kTileBytes);
+    const uint32_t desc_step = (uint32_t)kp.stage_bytes >> 4;
+    int stage = 0;
+    uint32_t phase = 0, at = 0;
+    bool ok = true;
+    for (int kt = kt0; kt < kt1; ++kt) {
+      if (!wait_at(full0 + 8 * stage, phase)) {
+        raise_status(&g_int8_status, ST_TIMEOUT);
+        *abort_flag = 1;
+        ok = false;
+        break;
       }
-      if (ok) commit_at(smem_u32(acc_full));
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < kBK / 32; ++kk)
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          umma_i8<1>(leader, tbase + (uint32_t)(g * ntile), a0 + at + g * (kTileBytes >> 4) + 2 * kk, b0 + at + 2 * kk, idesc,
+                     kk > 0 ? 1u : (uint32_t)(kt > kt0));
+      commit_at(leader, empty0 + 8 * stage);
+      at += desc_step;
+      if (++stage == stages) {
+        stage = 0;
+        at = 0;
+        phase ^= 1;
+      }
     }
+    if (ok) commit_at(leader, smem_u32(acc_full));
     __syncwarp();
     if (split > 1) cluster_wait();
   } else {
@@ -334,8 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (*abort_flag) {
     // let copies and MMAs already issued finish before the memory goes away
-    if (threadIdx.x == 32) {
-      umma_commit(drain);
+    if (warp == 1) {
+      commit_at(elect_lane(), smem_u32(drain));
       mbar_wait(drain, 0);
     }
     if (threadIdx.x == 0) {

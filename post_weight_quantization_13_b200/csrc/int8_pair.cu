@@ -61,11 +61,13 @@ struct PairMaps {
 
 // A tile into this CTA's shared memory, counted on a barrier of the pair
 // given by its cluster address.
-__device__ __forceinline__ void load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+__device__ __forceinline__ void load_pair(uint32_t leader, uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
+                                          int y) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-      "l"(map), "r"(bar), "r"(x), "r"(y)
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "@p cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(y), "r"(leader)
       : "memory");
 }
 // Arrive on a barrier of the pair.  What it orders are reads of tensor memory,
@@ -125,7 +127,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* epilogue_abort = abort_flag + 1;  // written and read between the epilogue warps' barriers only
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
   const int half = kp.bn / 2;  // channels a CTA loads
 
@@ -164,40 +166,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   const uint32_t stage0 = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
   if (warp == 0) {
-    if (lane == 0) {
-      const int stages = kp.stages, stage_bytes = kp.stage_bytes, ktiles = kp.ktiles;
-      const uint32_t bytes = 2u * (uint32_t)(kATile + half * kBK);  // of both CTAs
-      const uint32_t pair_full0 = map_to_rank(full0, 0);
-      const CUtensorMap* wmap = &maps.w[G == 2 ? rank : 0];
-      int stage = 0;
-      uint32_t phase = 1, at = stage0;
-      bool ok = true;
-      for (int tile = pair; tile < kp.tiles && ok; tile += kp.pairs) {
-        int mt, nt;
-        tile_at(kp, tile, &mt, &nt);
-        const int t0 = mt * 256 + rank * 128;
-        const int n0 = G == 2 ? nt * half : nt * kp.bn + rank * half;
-        for (int x = 0; x < ktiles * kBK; x += kBK) {
-          if (!wait_at(empty0 + 8 * stage, phase)) {
-            raise_status(kp.status, ST_TIMEOUT);
-            *abort_flag = 1;
-            ok = false;
-            break;
-          }
-          if (rank == 0) expect_at(full0 + 8 * stage, bytes);
-          load_pair(at, &maps.x, pair_full0 + 8 * stage, x, t0);
-          load_pair(at + kATile, wmap, pair_full0 + 8 * stage, x, n0);
-          at += stage_bytes;
-          if (++stage == stages) {
-            stage = 0;
-            at = stage0;
-            phase ^= 1;
-          }
+    const uint32_t leader = elect_lane();
+    const int stages = kp.stages, stage_bytes = kp.stage_bytes, ktiles = kp.ktiles;
+    const uint32_t bytes = 2u * (uint32_t)(kATile + half * kBK);  // of both CTAs
+    const uint32_t pair_full0 = map_to_rank(full0, 0);
+    const CUtensorMap* wmap = &maps.w[G == 2 ? rank : 0];
+    int stage = 0;
+    uint32_t phase = 1, at = stage0;
+    bool ok = true;
+    for (int tile = pair; tile < kp.tiles && ok; tile += kp.pairs) {
+      int mt, nt;
+      tile_at(kp, tile, &mt, &nt);
+      const int t0 = mt * 256 + rank * 128;
+      const int n0 = G == 2 ? nt * half : nt * kp.bn + rank * half;
+      for (int x = 0; x < ktiles * kBK; x += kBK) {
+        if (!wait_at(empty0 + 8 * stage, phase)) {
+          raise_status(kp.status, ST_TIMEOUT);
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        if (rank == 0) expect_at(leader, full0 + 8 * stage, bytes);
+        load_pair(leader, at, &maps.x, pair_full0 + 8 * stage, x, t0);
+        load_pair(leader, at + kATile, wmap, pair_full0 + 8 * stage, x, n0);
+        at += stage_bytes;
+        if (++stage == stages) {
+          stage = 0;
+          at = stage0;
+          phase ^= 1;
         }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const uint32_t leader = elect_lane();
       const int stages = kp.stages, ktiles = kp.ktiles;
       const uint32_t idesc = idesc_i8(256, (uint32_t)kp.bn);
       const uint32_t a0 = desc_low(stage0), b0 = desc_low(stage0 + kATile), desc_step = (uint32_t)kp.stage_bytes >> 4;
@@ -221,10 +223,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          umma_i8<2>(d, a0 + at, b0 + at, idesc, kt > 0);
+          umma_i8<2>(leader, d, a0 + at, b0 + at, idesc, kt > 0);
 #pragma unroll
-          for (int kk = 1; kk < kBK / 32; ++kk) umma_i8<2>(d, a0 + at + 2 * kk, b0 + at + 2 * kk, idesc, 1u);
-          commit_pair_at(empty0 + 8 * stage);
+          for (int kk = 1; kk < kBK / 32; ++kk) umma_i8<2>(leader, d, a0 + at + 2 * kk, b0 + at + 2 * kk, idesc, 1u);
+          commit_pair_at(leader, empty0 + 8 * stage);
           at += desc_step;
           if (++stage == stages) {
             stage = 0;
@@ -232,7 +234,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             phase ^= 1;
           }
         }
-        if (ok) commit_pair_at(smem_u32(&acc_full[buf]));
+        if (ok) commit_pair_at(leader, smem_u32(&acc_full[buf]));
       }
     }
   } else {
@@ -357,9 +359,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 
   __syncwarp();
-  if (*abort_flag && threadIdx.x == 32 && rank == 0) {
+  if (*abort_flag && warp == 1 && rank == 0) {
     // let the MMAs already issued finish before the memory goes away
-    commit_pair_at(smem_u32(drain));
+    commit_pair_at(elect_lane(), smem_u32(drain));
     mbar_wait(drain, 0);
   }
   if (*abort_flag && threadIdx.x == 0) {  // and the copies
