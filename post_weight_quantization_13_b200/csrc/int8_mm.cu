@@ -229,21 +229,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     // sixteen tokens at a time, the quarter's two warps in turn
     if (split == 1) {
       // a token at a time, 32 neighbouring channels a warp
-      T* const col = (T*)kp.Y + (int64_t)t0 * kp.ldy + n;
+      const bool zeros = kp.wzero[0] || (G == 2 && kp.wzero[1]);
+      const Pair w0(ws[0][0]), w1(ws[G - 1][0]), b(bias[0]);
+      auto scale = [&](const float* v, const Pair& w, int z, int j, Pair* y) {  // four tokens
+        int a[4] = {__float_as_int(v[0]), __float_as_int(v[1]), __float_as_int(v[2]), __float_as_int(v[3])};
+        if (zeros) {
+          const int4 sum = *reinterpret_cast<const int4*>(tsum + j);
+          a[0] -= z * sum.x;
+          a[1] -= z * sum.y;
+          a[2] -= z * sum.z;
+          a[3] -= z * sum.w;
+        }
+        const float4 t = *reinterpret_cast<const float4*>(tscale + j);
+        y[0] = mul2(mul2(Pair((float)a[0], (float)a[1]), Pair(t.x, t.y)), w);
+        y[1] = mul2(mul2(Pair((float)a[2], (float)a[3]), Pair(t.z, t.w)), w);
+      };
 #pragma unroll 1
       for (int j0 = 16 * second; j0 < live; j0 += 32) {
-        float a[16], u[16];
-        tmem_ld16(tmem + (uint32_t)j0, a);
-        if (G == 2) tmem_ld16(tmem + (uint32_t)(ntile + j0), u);
+        float v[G][16];
+        Pair y[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int j = j0 + i;
-          float y = scaled(__float_as_int(a[i]), wz[0][0], tsum[j], tscale[j], ws[0][0]);
-          if (G == 2)
-            y = activate(y, kp.act) * scaled(__float_as_int(u[i]), wz[G - 1][0], tsum[j], tscale[j], ws[G - 1][0]);
-          else
-            y += bias[0];
-          if (j < live && n < kp.out) col[(int64_t)j * kp.ldy] = from_f32<T>(y);
+        for (int g = 0; g < G; ++g) tmem_ld16(tmem + (uint32_t)(g * ntile + j0), v[g]);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          scale(v[0] + i, w0, wz[0][0], j0 + i, y + i / 2);
+          if (G == 2) {
+            Pair u[2];
+            scale(v[G - 1] + i, w1, wz[G - 1][0], j0 + i, u);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float2 f = y[i / 2 + k].f();
+              y[i / 2 + k] = mul2(Pair(activate(f.x, kp.act), activate(f.y, kp.act)), u[k]);
+            }
+          } else {
+            y[i / 2] = add2(y[i / 2], b);
+            y[i / 2 + 1] = add2(y[i / 2 + 1], b);
+          }
+        }
+        T* col = (T*)kp.Y + (int64_t)(t0 + j0) * kp.ldy + n;
+        const int left = n < kp.out ? live - j0 : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 f = y[i].f();
+          if (2 * i < left) col[0] = from_f32<T>(f.x);
+          if (2 * i + 1 < left) col[kp.ldy] = from_f32<T>(f.y);
+          col += 2 * kp.ldy;
         }
       }
       tc_fence_before();
