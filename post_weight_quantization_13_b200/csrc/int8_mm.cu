@@ -387,16 +387,65 @@ struct Plan {
   int ntile, split;  // split kernel: tokens of a tile, CTAs that share its k
 };
 
+// The estimates below choose among the tilings of both kernels.  Microseconds,
+// from 220 products of 3 to 2600 tokens with in and out from 300 to 20000,
+// each timed in up to 30 tilings: the tiling they choose takes on average
+// 1.008 times the best one's time (at worst 1.24), one fixed tiling 1.2 to 2
+// times.  G: products that share the tokens.
+//
+// A pair's k-tile takes the larger of its MMAs (0.30, or 0.25 with 128
+// channels) and its share of what L2 delivers (16 TB/s); only the last tile's
+// epilogue shows, unless a tile's main loop is shorter.
+float pair_us(int G, int64_t tokens, int64_t ktiles, int64_t out, int bn, int sms) {
+  const int64_t tiles = (tokens + 255) / 256 * ((out + bn / G - 1) / (bn / G));
+  const int64_t pairs = std::min<int64_t>(tiles, sms / 2), waves = (tiles + sms / 2 - 1) / (sms / 2);
+  const float ktile = std::max(bn == 256 ? 0.30f : 0.25f, 2.f * (16384 + bn * 64) * pairs / 16e6f);
+  const float epilogue = bn == 256 ? 5.5f : 3.5f;
+  return 2.9f + epilogue + waves * ktiles * ktile + (waves - 1) * std::max(0.f, epilogue - ktiles * ktile);
+}
+
+// A CTA's k-tile: issuing it (0.11), its MMAs, its share of L2, or what one SM
+// takes in (171 GB/s).  Clusters of four and eight cannot fill every GPC: 132
+// and 104 of their CTAs fit at once.  Partial sums cost their way to the other
+// CTAs.
+float split_us(int G, int64_t tokens, int64_t ktiles, int64_t out, int ntile, int split, int sms) {
+  const int64_t ctas = (out + kTileM - 1) / kTileM * ((tokens + ntile - 1) / ntile) * split;
+  const int64_t fit = split == 4 ? sms * 132 / 148 : split == 8 ? sms * 104 / 148 : sms;
+  const int64_t waves = (ctas + fit - 1) / fit, k = (ktiles + split - 1) / split;
+  const float bytes = (float)(G * kTileBytes + ntile * kBK);
+  const float ktile = std::max(std::max(0.11f, G * ntile * 1.4e-3f),
+                               bytes * std::max(std::min<int64_t>(ctas, sms) / 16e6f, 1 / 171e3f));
+  const float epilogue = split == 1 ? 1.6f + 0.011f * ntile * (G == 2 ? 2.5f : 1.f)
+                                    : 2.6f + 0.024f * ntile * (G == 2 ? 1.3f : 1.f);
+  return 2.6f + waves * (k * ktile + epilogue);
+}
+
+int stages_of(int G, int ntile, int split) {
+  return (kSmem - kSmemFixed - (split > 1 ? G * ntile * kTileM * 4 : 0)) / (G * kTileBytes + ntile * kBK);
+}
+
 Plan make_plan(int G, int64_t tokens, int64_t in, int64_t out, int sms) {
-  Plan p = {};
-  p.pair = tokens > 512;
-  p.bn = 256;
-  p.ntile = (int)std::min<int64_t>(G == 2 ? 64 : 128, (tokens + 15) / 16 * 16);
   const int64_t ktiles = (in + kBK - 1) / kBK;
-  const int64_t tiles = ((out + kTileM - 1) / kTileM) * ((tokens + p.ntile - 1) / p.ntile);
-  p.split = 1;
-  while (p.split < kMaxSplit && tiles * p.split * 2 <= sms && ktiles >= p.split * 4) p.split *= 2;
-  return p;
+  const int most = kMaxNTile / G;  // tokens of a tile that tensor memory and registers take
+  Plan best = {};
+  float best_us = 1e30f;
+  auto offer = [&](const Plan& p, float us) {
+    if (us < best_us) best = p, best_us = us;
+  };
+  // tiles of 64, 128 and 256 tokens, and those that divide the tokens evenly
+  // into up to four
+  const int64_t round = (tokens + 15) / 16 * 16;
+  for (int i = 0; i < 7; ++i) {
+    const int64_t ntile = i < 3 ? std::min<int64_t>(round, 64 << i) : ((tokens + i - 3) / (i - 2) + 15) / 16 * 16;
+    if (ntile > most) continue;
+    for (int split = 1; split <= kMaxSplit; split *= 2) {
+      if (split > 1 && (ktiles < 2 * split || stages_of(G, (int)ntile, split) < 3)) break;
+      offer({false, 0, (int)ntile, split}, split_us(G, tokens, ktiles, out, (int)ntile, split, sms));
+    }
+  }
+  if (tokens > 64)  // a pair's tile has 256 tokens
+    for (int bn = 128; bn <= 256; bn *= 2) offer({true, bn, 0, 0}, pair_us(G, tokens, ktiles, out, bn, sms));
+  return best;
 }
 
 // ------------------------------------------------------------------- host
@@ -476,7 +525,7 @@ cudaError_t run_split(MmParams kp, const gptq_int8_tokens_t* x, const gptq_int8_
   // The stages fill shared memory, so no two CTAs of these kernels share an
   // SM: a CTA that waits for tensor memory held by another could otherwise
   // hold up that one's cluster.
-  kp.stages = std::min(12, (kSmem - kSmemFixed - kp.push_bytes) / kp.stage_bytes);
+  kp.stages = std::min(12, stages_of(G, kp.ntile, kp.split));
   SplitMaps maps;
   std::memset(&maps, 0, sizeof(maps));
   for (int g = 0; g < G; ++g)
