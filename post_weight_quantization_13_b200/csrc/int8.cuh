@@ -209,6 +209,15 @@ __device__ __forceinline__ void tma_load_at(uint32_t leader, uint32_t dst, const
       "l"(map), "r"(bar), "r"(x), "r"(y), "r"(leader)
       : "memory");
 }
+// Untiled: bytes (a multiple of 16, possibly 0) from a 16-byte aligned address.
+__device__ __forceinline__ void bulk_load_at(uint32_t leader, uint32_t dst, const void* src, uint32_t bytes,
+                                             uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.and.b32 q, %2, 0, p;\n\t"
+      "@q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "r"(leader)
+      : "memory");
+}
 // K-major operand with 128-byte swizzling (see smem_desc_k_sw128): the low
 // word holds the address >> 4, the high word is the same for all.
 constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);

@@ -563,15 +563,12 @@ cudaError_t run(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const g
   return run_split<G>(kp, x, w, yt, plan, follows, st);
 }
 
-// Whether the rows kernel (int8_rows.cu) takes a product.
-bool few(int64_t tokens) { return tokens <= 2; }
-
 // follows: the kernel launched before on st is the quantizer that wrote x, and
 // this one may be set up while it runs.
 cudaError_t multiply(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, const gptq_int8_layer_t* const (&w)[2],
                      int64_t out, const float* bias, int act, void* Y, gptq_dtype_t yt, int64_t ldy, bool follows,
                      cudaStream_t st) {
-  if (few(tokens)) return rows_int8(nullptr, 0, 0, x, tokens, in, w, out, bias, act, Y, yt, ldy, st);
+  if (rows_int8_takes(tokens, in)) return rows_int8(nullptr, 0, 0, x, tokens, in, w, out, bias, act, Y, yt, ldy, st);
   const Plan plan = make_plan(w[1] ? 2 : 1, tokens, in, out, device_info().sms);
   if (plan.pair) {
     uint32_t* status = nullptr;
@@ -612,14 +609,14 @@ gptq_status_t matmul_int8_gated(const gptq_int8_tokens_t* x, int64_t tokens, int
 }
 
 size_t linear_int8_ws_bytes(int64_t tokens, int64_t in) {
-  return few(tokens) ? 0 : TokenScratch(nullptr, tokens, in).bytes;
+  return rows_int8_takes(tokens, in) ? 0 : TokenScratch(nullptr, tokens, in).bytes;
 }
 
 gptq_status_t linear_int8(const void* X, gptq_dtype_t xt, int64_t tokens, int64_t in, int64_t ldx,
                           const gptq_int8_layer_t* w, const gptq_int8_layer_t* up, int64_t out, const float* bias,
                           int act, void* Y, gptq_dtype_t yt, int64_t ldy, void* ws, cudaStream_t st) {
   const gptq_int8_layer_t* const layers[2] = {w, up};
-  if (few(tokens)) {
+  if (rows_int8_takes(tokens, in)) {
     CUDA_TRY(rows_int8(X, xt, ldx, nullptr, tokens, in, layers, out, bias, act, Y, yt, ldy, st));
     return GPTQ_OK;
   }

@@ -2,17 +2,19 @@
 // the gated pair, taking the tokens in 8 bits or in 16/32 (then each block
 // quantizes them itself: one launch, no scratch).
 //
-// What bounds it: the weights, in * out bytes once; arithmetic is a fifth of
-// what the SMs can do at that rate.  So the kernel keeps as many weight bytes
-// in flight as it can.  A block owns a contiguous range of channels and its
-// 256 threads split k: a thread's 16 columns of up to eight weight rows are
-// one batch of eight independent 16-byte loads, and the next batch is loaded
-// while this one is multiplied (dp4a) against the thread's own columns of the
-// tokens, which it keeps in shared memory for itself.  Every row of a batch
-// is read by the block as one contiguous run, the channels divide evenly over
-// the SMs whatever their number, and a channel's sum needs no more than a
-// transposed warp reduction (N values in N - 1 + log2(32 / N) exchanges) and
-// one exchange between the eight warps.
+// What bounds it: the weights, in * out bytes once.  So they stream through a
+// ring of shared memory, a few rows a slot, by bulk copies that a warp of its
+// own issues from the first cycles on: some 180 KB are in flight on every SM
+// whatever the rest of the block does.  (With rows loaded straight to
+// registers, two blocks an SM and 64 KB in flight, one token of 11008 x 4096
+// took 13.9 us, now 10.8; of the gated 4096 x 11008 20.4, now 18.0, where the
+// bytes alone take 14.)  A block owns a contiguous range of channels, which
+// divide evenly over the SMs whatever their number.  Two groups of 256 threads
+// take batches of eight rows in turn, one at its sums while the other
+// multiplies.  A group's threads split k: each multiplies (dp4a) its own
+// columns of the rows with its own columns of the tokens.  A row's sum then
+// costs its share of one transposed warp reduction for the batch (N values in
+// N - 1 + log2(32 / N) exchanges) and of one exchange between the warps.
 #include <algorithm>
 
 #include "gemm.cuh"
@@ -22,10 +24,14 @@
 namespace gptq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;          // of a group, whose threads split k
 constexpr int kWarps = kThreads / 32;
-constexpr int kLoads = 8;              // weight vectors a thread has in flight per step
+constexpr int kGroups = 2;             // that take the batches in turn
+constexpr int kBatch = 8;              // weight rows of a reduction
 constexpr int kSlice = kThreads * 16;  // columns of one step
+constexpr int kMaxSteps = 3;           // in <= 12288: two batches of the widest rows fill the ring
+constexpr int kMaxSlots = 40;          // of the ring
+constexpr int kSmem = 227 * 1024 - 6 * 1024;  // dynamic shared memory; the rest is the static arrays'
 
 struct RowsParams {
   const void* x;
@@ -43,6 +49,8 @@ struct RowsParams {
   int64_t ldy;
   int tokens, out, in, act;
   int rows;  // the most channels a block owns
+  int slots, slot_bytes, group, row_bytes, dense;
+  uint32_t* status;
   int vec;  // x's rows start on 16-byte boundaries
 };
 
@@ -94,26 +102,31 @@ __device__ __forceinline__ Raw8<X> load_columns(const X* __restrict__ row, int c
 }
 
 // The block's T tokens into codes (each thread its own columns), their scales
-// and sums into tscale and tsum.
-template <typename X, int T>
+// and sums into tscale and tsum.  The loads are issued before `start` lets the
+// weights flow, behind whose 180 KB per SM they would queue for microseconds.
+template <typename X, int T, typename Start>
 __device__ __forceinline__ void quantize_block(const RowsParams& kp, int4* codes, int steps, float* tscale, int* tsum,
-                                               uint32_t (*exchange)[T]) {
+                                               uint32_t (*exchange)[T], Start start) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int chunks = 2 * steps;  // of eight columns
+  Raw8<X> raw[T][2 * kMaxSteps];
+#pragma unroll
+  for (int t = 0; t < T; ++t)
+#pragma unroll
+    for (int s = 0; s < 2 * kMaxSteps; ++s)
+      raw[t][s] = t < kp.tokens ? load_columns((const X*)kp.x + t * kp.ldx,
+                                               (s >> 1) * kSlice + 16 * (int)threadIdx.x + 8 * (s & 1), kp.in, kp.vec)
+                                : zero8<X>();
+  if (threadIdx.x < T) tsum[threadIdx.x] = 0;
+  start();
 #pragma unroll
   for (int t = 0; t < T; ++t) {
     uint32_t top = 0u;
-    if (t < kp.tokens) {
-#pragma unroll 4
-      for (int s = 0; s < chunks; ++s)
-        top = magnitude(load_columns((const X*)kp.x + t * kp.ldx, (s >> 1) * kSlice + 16 * (int)threadIdx.x + 8 * (s & 1),
-                                     kp.in, kp.vec), top);
-    }
+#pragma unroll
+    for (int s = 0; s < 2 * kMaxSteps; ++s) top = magnitude(raw[t][s], top);
     top = __reduce_max_sync(0xffffffffu, magnitude_bits<X>(top));
     if (lane == 0) exchange[warp][t] = top;
   }
-  if (threadIdx.x < T) tsum[threadIdx.x] = 0;
-  __syncthreads();
+  named_bar_sync(1, kThreads);
 #pragma unroll
   for (int t = 0; t < T; ++t) {
     uint32_t top = 0u;
@@ -121,19 +134,19 @@ __device__ __forceinline__ void quantize_block(const RowsParams& kp, int4* codes
     for (int w = 0; w < kWarps; ++w) top = max(top, exchange[w][t]);
     const TokenScale scale(top);
     int total = 0;
-#pragma unroll 2
-    for (int s = 0; s < chunks; ++s) {  // the second reading hits L1
-      uint2 c = make_uint2(0u, 0u);
-      if (t < kp.tokens) {
-        const Raw8<X> r = load_columns((const X*)kp.x + t * kp.ldx,
-                                       (s >> 1) * kSlice + 16 * (int)threadIdx.x + 8 * (s & 1), kp.in, kp.vec);
+#pragma unroll
+    for (int s = 0; s < kMaxSteps; ++s) {
+      if (s >= steps) break;
+      uint2 c[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
         Pair f[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = get2(r, i);
-        c = scale.codes(f);
-        total = __dp4a((int)c.x, 0x01010101, __dp4a((int)c.y, 0x01010101, total));
+        for (int i = 0; i < 4; ++i) f[i] = get2(raw[t][2 * s + h], i);
+        c[h] = scale.codes(f);
+        total = __dp4a((int)c[h].x, 0x01010101, __dp4a((int)c[h].y, 0x01010101, total));
       }
-      reinterpret_cast<uint2*>(codes + (t * steps + (s >> 1)) * kThreads + threadIdx.x)[s & 1] = c;
+      codes[(t * steps + s) * kThreads + threadIdx.x] = make_int4((int)c[0].x, (int)c[0].y, (int)c[1].x, (int)c[1].y);
     }
     total = __reduce_add_sync(0xffffffffu, total);
     if (lane == 0) atomicAdd(&tsum[t], total);
@@ -142,123 +155,219 @@ __device__ __forceinline__ void quantize_block(const RowsParams& kp, int4* codes
 }
 
 template <int G, int T>
-__global__ void __launch_bounds__(kThreads, 2) int8_rows_kernel(const __grid_constant__ RowsParams kp) {
-  constexpr int R = kLoads / G;       // channels of a batch
-  constexpr int N = kLoads * T;       // sums of a batch, [g][channel][token]
-  extern __shared__ int4 codes[];     // [T][steps][thread]
+__global__ void __launch_bounds__(kGroups * kThreads + 32, 1) int8_rows_kernel(const __grid_constant__ RowsParams kp) {
+  constexpr int R = kBatch / G;  // channels of a batch
+  constexpr int N = kBatch * T;  // sums of a batch, [g][channel][token]
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float tscale[T];
   __shared__ int tsum[T];
   __shared__ uint32_t exchange[kWarps][T];
-  __shared__ int sums[2][kWarps][N];
+  __shared__ int sums[kGroups][2][kWarps][N];
+  __shared__ uint64_t full[kMaxSlots], empty[kMaxSlots];
+
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
+  const int steps = (kp.in + kSlice - 1) / kSlice, slots = kp.slots, slot_bytes = kp.slot_bytes;
+  uint8_t* const ring = smem;                                          // [slots][slot_bytes]
+  int4* const codes = (int4*)(smem + (size_t)slots * slot_bytes);      // [T][steps][thread]
   // the block's channels' scales, zeros and bias: fetched once up front, since
   // a load in a batch's epilogue would hold up the whole block for its latency
-  float* const wscale = (float*)(codes + (size_t)T * ((kp.in + kSlice - 1) / kSlice) * kThreads);  // [G][rows]
-  int* const wzero = (int*)(wscale + G * kp.rows);                                                  // [G][rows]
-  float* const bias = (float*)(wzero + G * kp.rows);                                                // [rows]
-
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int steps = (kp.in + kSlice - 1) / kSlice;
+  float* const wscale = (float*)(codes + (size_t)T * steps * kThreads);  // [G][rows]
+  int* const wzero = (int*)(wscale + G * kp.rows);                       // [G][rows]
+  float* const bias = (float*)(wzero + G * kp.rows);                     // [rows]
   const int n_begin = (int)((int64_t)kp.out * blockIdx.x / gridDim.x);
   const int n_end = (int)((int64_t)kp.out * (blockIdx.x + 1) / gridDim.x);
   const int batches = (n_end - n_begin + R - 1) / R;
 
-  // The loads of one step: a batch's rows at the thread's columns.  Rows past
-  // the range repeat its last one; their sums are not used.
-  auto load = [&](int4 (&w)[kLoads], int batch, int step) {
-    const int k = step * kSlice + 16 * (int)threadIdx.x;
-    const int n0 = n_begin + batch * R;
-    const int left = kp.in - k;
-    if (left >= 16 && n0 + R <= n_end) {
+  // A slot: `group` rows of each of the batch's projections, one after another
+  // at row_bytes.
+  const int group = kp.group, row_bytes = kp.row_bytes;
+  if (warp == kGroups * kWarps) {
+    // ------------------------------------------------------------ producer
+    for (int s = lane; s < slots; s += 32) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kWarps);
+    }
+    fence_mbar_init();
+    __syncwarp();
+    named_bar_sync(2, kThreads + 32);
+    const uint32_t leader = elect_lane();
+    const uint32_t ring0 = smem_u32(ring), full0 = smem_u32(full), empty0 = smem_u32(empty);
+    int slot = 0;
+    uint32_t phase = 1;
+    for (int c = 0; c < n_end - n_begin; c += group) {
+      if (!wait_at(empty0 + 8 * slot, phase)) {
+        raise_status(kp.status, ST_TIMEOUT);
+        // let the copies under way land before the block can end
+        const uint64_t start = globaltimer();
+        while (globaltimer() - start < 1000000ull) {
+        }
+        break;
+      }
+      const int n = n_begin + c, rows = min(group, n_end - n);
+      // whole 16-byte units of each row; the last row's storage may end inside one
+      const bool last = n + rows == kp.out;
+      const uint32_t row16 = (uint32_t)(kp.in + 15) & ~15u, tail = last ? (uint32_t)kp.in & ~15u : row16;
+      expect_at(leader, full0 + 8 * slot,
+                kp.dense ? G * ((rows - 1) * (uint32_t)row_bytes + tail) : G * ((rows - 1) * row16 + tail));
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const int8_t* p = kp.w[g] + n0 * kp.ldw[g] + k;
-#pragma unroll
-        for (int i = 0; i < R; ++i, p += kp.ldw[g]) w[g * R + i] = __ldg(reinterpret_cast<const int4*>(p));
+        const uint32_t at = ring0 + slot * kp.slot_bytes + g * group * row_bytes;
+        const int8_t* from = kp.w[g] + n * kp.ldw[g];
+        if (kp.dense) {  // rows follow one another as the slot wants them
+          bulk_load_at(leader, at, from, (rows - 1) * (uint32_t)row_bytes + tail, full0 + 8 * slot);
+        } else {
+          for (int r = 0; r < rows; ++r)
+            bulk_load_at(leader, at + r * row_bytes, from + r * kp.ldw[g], r + 1 < rows ? row16 : tail,
+                         full0 + 8 * slot);
+        }
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        w[i] = left > 0 ? load16(kp.w[i / R] + min(n0 + i % R, n_end - 1) * kp.ldw[i / R] + k, left)
-                        : make_int4(0, 0, 0, 0);
-    }
-  };
-
-  int4 w[kLoads];
-  load(w, 0, 0);  // in flight while the tokens are quantized
-  for (int i = threadIdx.x; i < n_end - n_begin; i += kThreads) {
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      wscale[g * kp.rows + i] = __ldg(kp.wscale[g] + n_begin + i);
-      wzero[g * kp.rows + i] = kp.wzero[g] ? __ldg(kp.wzero[g] + n_begin + i) : 0;
-    }
-    bias[i] = G == 1 && kp.bias ? __ldg(kp.bias + n_begin + i) : 0.f;
-  }
-  if (kp.xt < 0) {
-    if (threadIdx.x < T) {
-      tscale[threadIdx.x] = threadIdx.x < kp.tokens ? kp.tscale[threadIdx.x] : 0.f;
-      tsum[threadIdx.x] = threadIdx.x < kp.tokens ? kp.tsum[threadIdx.x] : 0;
-    }
-    for (int t = 0; t < T; ++t)
-      for (int s = 0; s < steps; ++s) {
-        const int k = s * kSlice + 16 * (int)threadIdx.x;
-        codes[(t * steps + s) * kThreads + threadIdx.x] =
-            t < kp.tokens && k < kp.in ? load16((const int8_t*)kp.x + t * kp.ldx + k, kp.in - k)
-                                       : make_int4(0, 0, 0, 0);
+      if (++slot == slots) {
+        slot = 0;
+        phase ^= 1;
       }
-  } else if (kp.xt == GPTQ_F16) {
-    quantize_block<__half, T>(kp, codes, steps, tscale, tsum, exchange);
-  } else if (kp.xt == GPTQ_BF16) {
-    quantize_block<__nv_bfloat16, T>(kp, codes, steps, tscale, tsum, exchange);
+    }
+    __syncwarp();
   } else {
-    quantize_block<float, T>(kp, codes, steps, tscale, tsum, exchange);
-  }
-
-  for (int batch = 0; batch < batches; ++batch) {
-    int acc[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0;
-    for (int step = 0; step < steps; ++step) {
-      int4 next[kLoads];
-      const bool last = step + 1 == steps;
-      if (!last || batch + 1 < batches) load(next, batch + (last ? 1 : 0), last ? 0 : step + 1);
-#pragma unroll
-      for (int t = 0; t < T; ++t) {
-        const int4 x = codes[(t * steps + step) * kThreads + threadIdx.x];
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) acc[i * T + t] = dot16(w[i], x, acc[i * T + t]);
-      }
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) w[i] = next[i];
-    }
-    const int sum = warp_sums<N>(acc);
-    if (lane % (32 / N) == 0) sums[batch & 1][warp][lane / (32 / N)] = sum;
-    // Also orders the tokens' scales and sums before their first use.  The
-    // other half of sums is written before the next barrier, this one after
-    // it, when its readers below are done.
-    __syncthreads();
-    if (threadIdx.x < R * T) {
-      const int t = threadIdx.x % T, n = n_begin + batch * R + (int)threadIdx.x / T;
-      if (t < kp.tokens && n < n_end) {
-        float y[G];
+    const int who = warp / kWarps, tid = (int)threadIdx.x & (kThreads - 1);
+    auto start = [&] { named_bar_sync(2, kThreads + 32); };
+    auto vectors = [&] {
+      for (int i = threadIdx.x; i < n_end - n_begin; i += kGroups * kThreads) {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          int total = 0;
-#pragma unroll
-          for (int v = 0; v < kWarps; ++v) total += sums[batch & 1][v][g * R * T + threadIdx.x];
-          y[g] = scaled(total, wzero[g * kp.rows + n - n_begin], tsum[t], tscale[t], wscale[g * kp.rows + n - n_begin]);
+          wscale[g * kp.rows + i] = __ldg(kp.wscale[g] + n_begin + i);
+          wzero[g * kp.rows + i] = kp.wzero[g] ? __ldg(kp.wzero[g] + n_begin + i) : 0;
         }
-        float o = y[0];
-        if (G == 2)
-          o = activate(y[0], kp.act) * y[G - 1];
-        else
-          o += bias[n - n_begin];
-        const int64_t at = t * kp.ldy + n;
-        if (kp.yt == GPTQ_F16)
-          ((__half*)kp.Y)[at] = from_f32<__half>(o);
-        else if (kp.yt == GPTQ_BF16)
-          ((__nv_bfloat16*)kp.Y)[at] = from_f32<__nv_bfloat16>(o);
-        else
-          ((float*)kp.Y)[at] = o;
+        bias[i] = G == 1 && kp.bias ? __ldg(kp.bias + n_begin + i) : 0.f;
+      }
+    };
+    if (who > 0) {
+      // the first group brings the tokens
+    } else if (kp.xt < 0) {
+      if (threadIdx.x < T) {
+        tscale[threadIdx.x] = threadIdx.x < kp.tokens ? kp.tscale[threadIdx.x] : 0.f;
+        tsum[threadIdx.x] = threadIdx.x < kp.tokens ? kp.tsum[threadIdx.x] : 0;
+      }
+      int4 x[T][kMaxSteps];
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int s = 0; s < kMaxSteps; ++s) {
+          const int k = s * kSlice + 16 * (int)threadIdx.x;
+          x[t][s] = t < kp.tokens && k < kp.in ? load16((const int8_t*)kp.x + t * kp.ldx + k, kp.in - k)
+                                               : make_int4(0, 0, 0, 0);
+        }
+      start();
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int s = 0; s < kMaxSteps; ++s)
+          if (s < steps) codes[(t * steps + s) * kThreads + threadIdx.x] = x[t][s];
+    } else if (kp.xt == GPTQ_F16) {
+      quantize_block<__half, T>(kp, codes, steps, tscale, tsum, exchange, start);
+    } else if (kp.xt == GPTQ_BF16) {
+      quantize_block<__nv_bfloat16, T>(kp, codes, steps, tscale, tsum, exchange, start);
+    } else {
+      quantize_block<float, T>(kp, codes, steps, tscale, tsum, exchange, start);
+    }
+    vectors();
+    named_bar_sync(3, kGroups * kThreads);
+
+    const uint32_t full0 = smem_u32(full);
+    const int per_batch = R / group;  // slots
+    int slot = 0;
+    uint32_t phase = 0;
+    auto advance = [&](int by) {
+      slot += by;
+      while (slot >= slots) {
+        slot -= slots;
+        phase ^= 1;
+      }
+    };
+    advance(who * per_batch);
+    bool gave_up = false;  // after a wait that gave up the block runs on without waiting, on whatever is there
+    int half = 0;
+    for (int batch = who; batch < batches; batch += kGroups, half ^= 1) {
+      int acc[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i] = 0;
+      // the batch's slots; its rows' places in them (rows past the range
+      // repeat its last one: their sums are not used)
+      const int first = batch * R, rows = min(R, n_end - n_begin - first);
+      const int4* row[kBatch];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int at = r & (group - 1);  // a batch is whole slots
+        if (at == 0 && r < rows) {
+          if (r > 0) advance(1);
+          if (!gave_up && !wait_at(full0 + 8 * slot, phase)) {
+            gave_up = true;
+            raise_status(kp.status, ST_TIMEOUT);
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          row[g * R + r] =
+              r < rows ? (const int4*)(ring + (size_t)slot * kp.slot_bytes + (g * group + at) * row_bytes) + tid
+                       : row[g * R + r - 1];
+      }
+      for (int step = 0; step < steps; ++step) {
+        const int k = step * kSlice + 16 * tid;
+        if (k >= kp.in) break;
+        int4 w[kBatch], x[T];
+#pragma unroll
+        for (int t = 0; t < T; ++t) x[t] = codes[(t * steps + step) * kThreads + tid];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) w[i] = row[i][step * kThreads];
+        if (k + 16 > kp.in && n_begin + first + rows == kp.out)  // the last row's tail was not copied
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const int4 tail = load16(kp.w[g] + (int64_t)(kp.out - 1) * kp.ldw[g] + k, kp.in - k);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+              if (r >= rows - 1) w[g * R + r] = tail;
+          }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+          for (int t = 0; t < T; ++t) acc[i * T + t] = dot16(w[i], x[t], acc[i * T + t]);
+      }
+      __syncwarp();
+      // back from the batch's last slot to its first
+      const int held = (rows + group - 1) / group;
+      for (int j = 0; j < held; ++j) {
+        const int s = slot - j + (slot < j ? slots : 0);
+        if (lane == 0) mbar_arrive(&empty[s]);
+      }
+      advance(per_batch - (held - 1) + (kGroups - 1) * per_batch);
+      const int sum = warp_sums<N>(acc);
+      if (lane % (32 / N) == 0) sums[who][half][warp % kWarps][lane / (32 / N)] = sum;
+      // The other half of sums is written before the group's next barrier, this
+      // one after it, when its readers below are done.
+      named_bar_sync(4 + who, kThreads);
+      if (tid < R * T) {
+        const int t = tid % T, c = batch * R + tid / T, n = n_begin + c;
+        if (t < kp.tokens && n < n_end) {
+          float y[G];
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            int total = 0;
+#pragma unroll
+            for (int v = 0; v < kWarps; ++v) total += sums[who][half][v][g * R * T + tid];
+            y[g] = scaled(total, wzero[g * kp.rows + c], tsum[t], tscale[t], wscale[g * kp.rows + c]);
+          }
+          float o = y[0];
+          if (G == 2)
+            o = activate(y[0], kp.act) * y[G - 1];
+          else
+            o += bias[c];
+          const int64_t at = t * kp.ldy + n;
+          if (kp.yt == GPTQ_F16)
+            ((__half*)kp.Y)[at] = from_f32<__half>(o);
+          else if (kp.yt == GPTQ_BF16)
+            ((__nv_bfloat16*)kp.Y)[at] = from_f32<__nv_bfloat16>(o);
+          else
+            ((float*)kp.Y)[at] = o;
+        }
       }
     }
   }
@@ -266,25 +375,40 @@ __global__ void __launch_bounds__(kThreads, 2) int8_rows_kernel(const __grid_con
 
 template <int G, int T>
 cudaError_t launch(RowsParams& kp, cudaStream_t st, int sms) {
-  // two blocks an SM, none without a batch of its own
-  const int grid = std::min(2 * sms, (kp.out + kLoads / G - 1) / (kLoads / G));
+  const int grid = std::min(sms, kp.out);
   kp.rows = (kp.out + grid - 1) / grid;
   const int steps = (kp.in + kSlice - 1) / kSlice;
-  const int smem = T * steps * kThreads * 16 + (2 * G + 1) * kp.rows * 4;
+  const int fixed = T * steps * kThreads * 16 + (2 * G + 1) * kp.rows * 4;
+  // Slots of up to 32 KB (a copy's issue takes as long as some KB of it): 1, 2,
+  // 4 or 8 channels, as a batch is whole slots.  Rows that lie closely one
+  // after another come in one copy, padding and all.
+  kp.dense = 1;
+  for (int g = 0; g < G; ++g) kp.dense &= kp.ldw[g] == kp.ldw[0] && kp.ldw[g] <= kp.in + 127;
+  kp.row_bytes = kp.dense ? (int)kp.ldw[0] : (kp.in + 15) / 16 * 16;
+  kp.group = kBatch / G;
+  while (kp.group > 1 && G * kp.group * kp.row_bytes > 32768) kp.group /= 2;
+  kp.slot_bytes = (G * kp.group * kp.row_bytes + 127) / 128 * 128;
+  // at least two batches' (12288 wide, two tokens: 196 of the 198 KB left)
+  kp.slots = std::min(kMaxSlots, (kSmem - fixed) / kp.slot_bytes);
+  const int smem = fixed + kp.slots * kp.slot_bytes;
   const void* f = (const void*)int8_rows_kernel<G, T>;
-  cudaError_t e = ensure_smem_limit(f, smem);
+  cudaError_t e = ensure_smem_limit(f, kSmem);
   if (e != cudaSuccess) return e;
-  int8_rows_kernel<G, T><<<grid, kThreads, smem, st>>>(kp);
+  int8_rows_kernel<G, T><<<grid, kGroups * kThreads + 32, smem, st>>>(kp);
   note_launch();
   return cudaGetLastError();
 }
 
 }  // namespace
 
+bool rows_int8_takes(int64_t tokens, int64_t in) { return tokens <= 2 && in <= kMaxSteps * kSlice; }
+
 cudaError_t rows_int8(const void* x, int xt, int64_t ldx, const gptq_int8_tokens_t* tokens8, int64_t tokens, int64_t in,
                       const gptq_int8_layer_t* const (&w)[2], int64_t out, const float* bias, int act, void* Y,
                       gptq_dtype_t yt, int64_t ldy, cudaStream_t st) {
   RowsParams kp = {};
+  const cudaError_t e = int8_status_word(&kp.status);
+  if (e != cudaSuccess) return e;
   kp.x = tokens8 ? tokens8->q : x;
   kp.xt = tokens8 ? -1 : xt;
   kp.ldx = tokens8 ? tokens8->ldq : ldx;

@@ -91,7 +91,9 @@ size_t linear_int8_ws_bytes(int64_t tokens, int64_t in);
 gptq_status_t linear_int8(const void* X, gptq_dtype_t xt, int64_t tokens, int64_t in, int64_t ldx,
                           const gptq_int8_layer_t* w, const gptq_int8_layer_t* up, int64_t out, const float* bias,
                           int act, void* Y, gptq_dtype_t yt, int64_t ldy, void* ws, cudaStream_t st);
-// Both for at most two tokens (int8_rows.cu): tokens8, or x of type xt.
+// Both for one or two tokens of rows that fit (int8_rows.cu): tokens8, or x of
+// type xt.
+bool rows_int8_takes(int64_t tokens, int64_t in);
 cudaError_t rows_int8(const void* x, int xt, int64_t ldx, const gptq_int8_tokens_t* tokens8, int64_t tokens, int64_t in,
                       const gptq_int8_layer_t* const (&w)[2], int64_t out, const float* bias, int act, void* Y,
                       gptq_dtype_t yt, int64_t ldy, cudaStream_t st);
