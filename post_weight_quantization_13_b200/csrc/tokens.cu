@@ -27,11 +27,136 @@ constexpr int kStreamChunks = 2;         // chunks of eight elements a thread of
 constexpr int kStreamMin = 1024;         // elements of the narrowest rows the streaming kernels take
 constexpr int kSmemPerSm = 227 * 1024;
 
-// Chunk i of the thread's share of a row of d elements; zero past the end.
+// A thread's chunks of a row: eight neighbouring elements each.  Rows on 16-byte
+// boundaries are cut at multiples of eight.  Else (kShift: odd sizes, where
+// successive rows have every alignment) the cuts move to the row's 16-byte
+// boundaries, m elements before those multiples, so that all but a row's two
+// ends still go by 16-byte accesses for every operand aligned like the one m
+// was taken from, as contiguous tensors of one size are.  (Norms of
+// 8000 rows of 4001 bf16 by single elements: 120 to 150 us, now 81; 8192 rows
+// of 4096: 57.)
+template <bool kShift>
+struct Cut {
+  int m;
+  // For rows of d elements like this one, on threads that hold `slots`; 0 in
+  // the few cases where they do not hold the shift.
+  template <typename T>
+  __device__ __forceinline__ Cut(const T* row, int d, int slots) : m(kShift ? (int)((uintptr_t)row / sizeof(T)) & 7 : 0) {
+    if (d + m > slots) m = 0;
+  }
+  __device__ __forceinline__ int start(int i) const {
+    return 8 * (int)(threadIdx.x + i * blockDim.x) - (kShift ? m : 0);
+  }
+  static __device__ __forceinline__ bool inside(int e, int d) { return (!kShift || e >= 0) && e + 8 <= d; }
+  // Whether this operand's chunks lie on 16-byte boundaries.
+  template <typename T>
+  __device__ __forceinline__ bool fits(const T* row) const {
+    return !kShift || (((uintptr_t)row - m * sizeof(T)) & 15) == 0;
+  }
+};
+// The chunk that starts at element e (from -7 on) of a row of d elements, in
+// global or shared memory; zero outside the row.
+template <bool kShift, typename T>
+__device__ __forceinline__ Raw8<T> load_chunk(const Cut<kShift>& cut, const T* __restrict__ row, int e, int d) {
+  if constexpr (!kShift) {
+    return e < d ? load8(row + e, d - e, true) : zero8<T>();
+  } else {
+    if (cut.fits(row) && cut.inside(e, d)) return load8(row + e, 8, true);
+    Raw8<T> r = zero8<T>();
+    if (e >= d) return r;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (e + u < 0 || e + u >= d) continue;
+      if constexpr (sizeof(T) == 4)
+        r.w[u] = reinterpret_cast<const uint32_t*>(row)[e + u];
+      else
+        r.w[u / 2] |= (uint32_t)reinterpret_cast<const unsigned short*>(row)[e + u] << (16 * (u & 1));
+    }
+    return r;
+  }
+}
+// The same of a vector in global memory, whose own alignment seldom is the
+// rows': two 16-byte loads and a shift by the elements between.
+template <bool kShift, typename T>
+__device__ __forceinline__ Raw8<T> load_vector(const Cut<kShift>& cut, const T* __restrict__ p, int e, int d) {
+  if constexpr (kShift && sizeof(T) == 2) {
+    const int r = e & 7, at = e - r;
+    if (r && ((uintptr_t)p & 15) == 0 && at >= 0 && at + 16 <= d) {
+      const Raw8<T> a = load8(p + at, 8, true), b = load8(p + at + 8, 8, true);
+      uint32_t v[8] = {a.w[0], a.w[1], a.w[2], a.w[3], b.w[0], b.w[1], b.w[2], b.w[3]};
+#pragma unroll
+      for (int j = 0; j < 6; ++j) v[j] = r & 4 ? v[j + 2] : v[j];
+#pragma unroll
+      for (int j = 0; j < 5; ++j) v[j] = r & 2 ? v[j + 1] : v[j];
+      Raw8<T> o;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o.w[j] = __funnelshift_r(v[j], v[j + 1], (r & 1) * 16);
+      return o;
+    }
+  }
+  return load_chunk<kShift>(cut, p, e, d);
+}
+template <bool kShift, typename T>
+__device__ __forceinline__ void store_chunk(const Cut<kShift>& cut, T* __restrict__ row, int e, int d,
+                                            const Pair (&v)[4]) {
+  if constexpr (!kShift) {
+    if (e < d) store8(row + e, v, d - e, true);
+  } else {
+    if (cut.fits(row) && cut.inside(e, d)) {
+      store8(row + e, v, 8, true);
+      return;
+    }
+    if (e >= d) return;
+    alignas(16) T r[8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float2 f = v[u].f();
+      const float a[2] = {f.x, f.y};
+      round_n<2>(a, r + 2 * u);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (e + u >= 0 && e + u < d) row[e + u] = r[u];
+  }
+}
+// Eight codes from element e, a multiple of eight; q's rows start on 16-byte
+// boundaries.
+__device__ __forceinline__ void store_codes(int8_t* __restrict__ q, int e, int d, uint2 w) {
+  if (e + 8 <= d) {
+    *reinterpret_cast<uint2*>(q + e) = w;
+  } else {
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (e + u < d) q[e + u] = (int8_t)((u < 4 ? w.x : w.y) >> (8 * (u & 3)));
+  }
+}
+// Eight elements from e, a multiple of eight, of a row in shared memory that
+// begins anywhere: the 16-byte units it touches, shifted (units around the row
+// belong to its stage); zero past the row.
 template <typename T>
-__device__ __forceinline__ Raw8<T> load_chunk(const T* __restrict__ row, int i, int d, bool vec) {
-  const int c0 = 8 * (threadIdx.x + i * blockDim.x);
-  return c0 < d ? load8(row + c0, d - c0, vec) : zero8<T>();
+__device__ __forceinline__ Raw8<T> read_across(const T* row, int e, int d) {
+  Raw8<T> o = zero8<T>();
+  if constexpr (sizeof(T) == 2) {
+    if (e >= d) return o;
+    const int r = (int)((uintptr_t)row / 2) & 7;
+    const T* at = row + e - r;
+    const Raw8<T> a = load8(at, 8, true), b = load8(at + 8, 8, true);
+    uint32_t v[8] = {a.w[0], a.w[1], a.w[2], a.w[3], b.w[0], b.w[1], b.w[2], b.w[3]};
+#pragma unroll
+    for (int j = 0; j < 6; ++j) v[j] = r & 4 ? v[j + 2] : v[j];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) v[j] = r & 2 ? v[j + 1] : v[j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o.w[j] = __funnelshift_r(v[j], v[j + 1], (r & 1) * 16);
+    if (e + 8 > d)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o.w[j] = e + 2 * j + 1 < d ? o.w[j] : e + 2 * j < d ? o.w[j] & 0xffffu : 0u;
+  } else {
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (e + u < d) o.w[u] = reinterpret_cast<const uint32_t*>(row)[e + u];
+  }
+  return o;
 }
 
 // ------------------------------------------------------------ row reductions
@@ -81,46 +206,67 @@ struct RowReduce {
 
 // A row in registers, top its largest magnitude (fp32 bits) over this thread's
 // elements, to codes, scale and sum.
-template <int NV>
-__device__ __forceinline__ void quantize_row(const Pair (&v)[NV][4], uint32_t top, int d, RowReduce& red,
+// Shifted cuts: an aligned eight of codes comes from a chunk's last 8 - m and
+// its right neighbour's first m; a warp's last lane gets those through shared
+// memory (edge) behind the barrier of the codes' sum.
+template <int NV, bool kShift>
+__device__ __forceinline__ void quantize_row(const Cut<kShift>& cut, const Pair (&v)[NV][4], uint32_t top, int d,
+                                             RowReduce& red, uint64_t (&edge)[kShift ? 32 * NV : 1],
                                              int8_t* __restrict__ q, float* __restrict__ scale,
                                              int32_t* __restrict__ sum) {
   const TokenScale s(red.max_u32(top));
+  const int lane = threadIdx.x & 31, m = cut.m, warps = blockDim.x >> 5;
+  const int warp = (threadIdx.x >> 5) + warps * threadIdx.y;  // (several rows of one warp, or one row)
   int total = 0;
+  uint64_t last[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c0 = 8 * (threadIdx.x + i * blockDim.x);
-    if (c0 >= d) continue;
+    const int e = cut.start(i);
+    if (!kShift && e >= d) continue;
     const uint2 w = s.codes(v[i]);
     total = __dp4a((int)w.x, 0x01010101, __dp4a((int)w.y, 0x01010101, total));
-    if (c0 + 8 <= d) {
-      *reinterpret_cast<uint2*>(q + c0) = w;
+    if (!kShift || m == 0) {
+      if (e < d) store_codes(q, e, d, w);
     } else {
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (c0 + u < d) q[c0 + u] = (int8_t)((u < 4 ? w.x : w.y) >> (8 * (u & 3)));
+      const uint64_t own = (uint64_t)w.y << 32 | w.x, next = __shfl_down_sync(0xffffffffu, own, 1);
+      const uint64_t eight = own >> (8 * m) | next << (64 - 8 * m);
+      if (lane < 31 && e + m < d) store_codes(q, e + m, d, make_uint2((uint32_t)eight, (uint32_t)(eight >> 32)));
+      if (lane == 0) edge[32 * i + warp] = own;
+      last[i] = own;
     }
   }
+  if (kShift && warps == 1) __syncwarp();
   total = red.sum_s32(total);
+  if (kShift && m && lane == 31) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const bool inner = (threadIdx.x >> 5) + 1 < warps;
+      const uint64_t next = inner ? edge[32 * i + warp + 1] : i + 1 < NV ? edge[32 * (i + 1 < NV ? i + 1 : i) + warp + 1 - warps] : 0;
+      const uint64_t eight = last[i] >> (8 * m) | next << (64 - 8 * m);
+      const int e = cut.start(i) + m;
+      if (e < d) store_codes(q, e, d, make_uint2((uint32_t)eight, (uint32_t)(eight >> 32)));
+    }
+  }
   if (threadIdx.x == 0) {
     *scale = s.scale;
     *sum = total;
   }
 }
 
-template <typename T, int NV>
+template <typename T, int NV, bool kShift>
 __global__ void __launch_bounds__(1024) quantize_tokens_kernel(const T* __restrict__ X, int64_t tokens, int d,
                                                                int64_t ldx, int8_t* __restrict__ q, int64_t ldq,
-                                                               float* __restrict__ scale, int32_t* __restrict__ sum,
-                                                               bool vec) {
+                                                               float* __restrict__ scale, int32_t* __restrict__ sum) {
   __shared__ uint32_t buf[64];
+  __shared__ uint64_t edge[kShift ? 32 * NV : 1];
   grid_launch_dependents();  // a product behind this kernel sets up beside it
   const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= tokens) return;  // whole warps: rows of several per block are one warp wide
   RowReduce red(buf);
+  const Cut<kShift> cut(X + t * ldx, d, 8 * NV * (int)blockDim.x);
   Raw8<T> r[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) r[i] = load_chunk(X + t * ldx, i, d, vec);
+  for (int i = 0; i < NV; ++i) r[i] = load_chunk<kShift>(cut, X + t * ldx, cut.start(i), d);
   Pair v[NV][4];
   uint32_t top = 0;
 #pragma unroll
@@ -129,7 +275,7 @@ __global__ void __launch_bounds__(1024) quantize_tokens_kernel(const T* __restri
 #pragma unroll
     for (int u = 0; u < 4; ++u) v[i][u] = get2(r[i], u);
   }
-  quantize_row<NV>(v, magnitude_bits<T>(top), d, red, q + t * ldq, scale + t, sum + t);
+  quantize_row<NV, kShift>(cut, v, magnitude_bits<T>(top), d, red, edge, q + t * ldq, scale + t, sum + t);
 }
 
 // ------------------------------------------------------------------- norms
@@ -146,49 +292,51 @@ struct NormParams {
   int layer;
   int stages, stage_bytes;  // of the streaming kernel
   uint32_t* status;
-  // 16-byte access per operand
-  int vec_h, vec_y, vec_post_weight, vec_post_bias, vec_gate, vec_weight, vec_bias, vec_h_out, vec_x;
+  int aligned;  // every operand's rows start on 16-byte boundaries
 };
 
 // A norm's weight and bias (or a gate) at the thread's columns.  kEarly: held
 // in registers from the start, so that no load waits behind a statistic; else
 // fetched where they are used, for want of registers.
-template <typename T, int NV, bool kEarly>
+template <typename T, int NV, bool kEarly, bool kShift>
 struct Vector {
   const T* p;
-  int d, vec;
+  int d;
+  Cut<kShift> cut;
   Raw8<T> r[kEarly ? NV : 1];
-  __device__ __forceinline__ Vector(const void* p_, int d_, int vec_) : p((const T*)p_), d(d_), vec(vec_) {
+  __device__ __forceinline__ Vector(const Cut<kShift>& cut_, const void* p_, int d_) : p((const T*)p_), d(d_), cut(cut_) {
     if (kEarly && p) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) r[kEarly ? i : 0] = load_chunk(p, i, d, vec);
+      for (int i = 0; i < NV; ++i) r[kEarly ? i : 0] = load_vector<kShift>(cut, p, cut.start(i), d);
     }
   }
   __device__ __forceinline__ explicit operator bool() const { return p != nullptr; }
   __device__ __forceinline__ Raw8<T> chunk(int i) const {
-    return kEarly ? r[kEarly ? i : 0] : load_chunk(p, i, d, vec);
+    return kEarly ? r[kEarly ? i : 0] : load_vector<kShift>(cut, p, cut.start(i), d);
   }
 };
 
-// Zero past the row's end, so that nothing there reaches a statistic.
-template <int NV>
-__device__ __forceinline__ void clear_past(Pair (&v)[NV][4], int d) {
+// Zero outside the row, so that nothing there reaches a statistic.
+template <int NV, bool kShift>
+__device__ __forceinline__ void clear_past(const Cut<kShift>& cut, Pair (&v)[NV][4], int d) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c0 = 8 * (threadIdx.x + i * blockDim.x);
-    if (c0 + 8 <= d) continue;
+    const int e = cut.start(i);
+    if (cut.inside(e, d)) continue;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const float2 f = v[i][u].f();
-      v[i][u] = Pair(c0 + 2 * u < d ? f.x : 0.f, c0 + 2 * u + 1 < d ? f.y : 0.f);
+      const int a = e + 2 * u;
+      v[i][u] = Pair(a >= 0 && a < d ? f.x : 0.f, a + 1 >= 0 && a + 1 < d ? f.y : 0.f);
     }
   }
 }
 
 // The row without its mean where that is asked for, and 1 / sqrt(mean v^2 +
-// eps).  kTail: rows may end inside a chunk or leave threads without one.
-template <int NV, bool kTail>
-__device__ __forceinline__ float norm_statistic(Pair (&v)[NV][4], const NormParams& p, RowReduce& red) {
+// eps).
+template <int NV, bool kShift>
+__device__ __forceinline__ float norm_statistic(const Cut<kShift>& cut, Pair (&v)[NV][4], const NormParams& p,
+                                                RowReduce& red) {
   const float inv_d = 1.f / (float)p.d;
   if (p.layer) {
     Pair s(0.f);
@@ -201,7 +349,7 @@ __device__ __forceinline__ float norm_statistic(Pair (&v)[NV][4], const NormPara
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int u = 0; u < 4; ++u) v[i][u] = add2(v[i][u], mean);
-    clear_past(v, p.d);
+    clear_past<NV, kShift>(cut, v, p.d);
   }
   Pair s2(0.f);
 #pragma unroll
@@ -228,23 +376,20 @@ __device__ __forceinline__ void norm_apply(Pair (&v)[NV][4], float r, const V& w
   }
 }
 
-template <int NV, bool kTail, typename T>
-__device__ __forceinline__ void store_row(T* __restrict__ row, const Pair (&v)[NV][4], int d, bool vec) {
+template <int NV, bool kShift, typename T>
+__device__ __forceinline__ void store_row(const Cut<kShift>& cut, T* __restrict__ row, const Pair (&v)[NV][4], int d) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c0 = 8 * (threadIdx.x + i * blockDim.x);
-    if (c0 < d) store8(row + c0, v[i], kTail ? d - c0 : 8, kTail ? vec : true);
-  }
+  for (int i = 0; i < NV; ++i) store_chunk<kShift>(cut, row, cut.start(i), d, v[i]);
 }
 
 // One token: h' = alpha h + beta gate * post(y);  x = pre(h') in 16/32 bits
 // and/or int8.  The pre-norm works on h' before it is rounded to its stored
 // type.  h(i), y(i) and gate(i) give the operands' chunks; release() is called
 // once by every thread when the whole row has been read by all of them.
-template <typename T, typename H, int NV, bool kTail, typename LoadH, typename LoadY, typename LoadGate, typename V,
+template <typename T, typename H, int NV, bool kShift, typename LoadH, typename LoadY, typename LoadGate, typename V,
           typename B, typename Release>
-__device__ __forceinline__ void norm_token(const NormParams& p, int64_t t, RowReduce& red, LoadH h, LoadY y,
-                                           LoadGate gate, const V& post_weight, const B& post_bias, const V& weight,
+__device__ __forceinline__ void norm_token(const Cut<kShift>& cut, const NormParams& p, int64_t t, RowReduce& red,
+                                           uint64_t (&edge)[kShift ? 32 * NV : 1], LoadH h, LoadY y, LoadGate gate, const V& post_weight, const B& post_bias, const V& weight,
                                            const B& bias, Release release) {
   const int d = p.d;
   const Pair alpha(p.alpha);
@@ -257,7 +402,7 @@ __device__ __forceinline__ void norm_token(const NormParams& p, int64_t t, RowRe
 #pragma unroll
       for (int u = 0; u < 4; ++u) v[i][u] = get2(r, u);
     }
-    if (post_weight) norm_apply<NV>(v, norm_statistic<NV, kTail>(v, p, red), post_weight, post_bias);
+    if (post_weight) norm_apply<NV>(v, norm_statistic<NV, kShift>(cut, v, p, red), post_weight, post_bias);
     if (p.gate) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -280,15 +425,15 @@ __device__ __forceinline__ void norm_token(const NormParams& p, int64_t t, RowRe
       for (int u = 0; u < 4; ++u) v[i][u] = mul2(alpha, get2(r, u));
     }
   }
-  clear_past(v, d);
-  if (p.h_out) store_row<NV, kTail>((H*)p.h_out + t * p.ldh_out, v, d, p.vec_h_out);
+  clear_past<NV, kShift>(cut, v, d);
+  if (p.h_out) store_row<NV, kShift>(cut, (H*)p.h_out + t * p.ldh_out, v, d);
   if (!p.weight) return;
-  const float r = norm_statistic<NV, kTail>(v, p, red);
+  const float r = norm_statistic<NV, kShift>(cut, v, p, red);
   release();
   norm_apply<NV>(v, r, weight, bias);
-  if (p.x) store_row<NV, kTail>((T*)p.x + t * p.ldx, v, d, p.vec_x);
+  if (p.x) store_row<NV, kShift>(cut, (T*)p.x + t * p.ldx, v, d);
   if (p.q) {
-    clear_past(v, d);
+    clear_past<NV, kShift>(cut, v, d);
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -297,36 +442,46 @@ __device__ __forceinline__ void norm_token(const NormParams& p, int64_t t, RowRe
         const float2 f = v[i][u].f();
         top = max(max(top, __float_as_uint(f.x) & 0x7fffffffu), __float_as_uint(f.y) & 0x7fffffffu);
       }
-    quantize_row<NV>(v, top, d, red, p.q + t * p.ldq, p.scale + t, p.sum + t);
+    quantize_row<NV, kShift>(cut, v, top, d, red, edge, p.q + t * p.ldq, p.scale + t, p.sum + t);
   }
 }
 
 // A row a warp or a block, every operand straight to registers: few tokens,
 // narrow rows, unaligned rows.
-template <typename T, typename H, int NV>
+template <typename T, typename H, int NV, bool kShift>
 __global__ void __launch_bounds__(1024) norm_tokens_kernel(const __grid_constant__ NormParams p) {
   __shared__ uint32_t buf[64];
+  __shared__ uint64_t edge[kShift ? 32 * NV : 1];
   const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= p.tokens) return;
   const int d = p.d;
   RowReduce red(buf);
-  using V = Vector<T, NV, NV == 1>;
+  using V = Vector<T, NV, NV == 1, kShift>;
+  const H* const hr = (const H*)p.h + t * p.ldh;
+  const T* const yr = p.y ? (const T*)p.y + t * p.ldy : nullptr;
+  const T* const gr = p.gate ? (const T*)p.gate + t * p.ldgate : nullptr;
+  const int slots = 8 * NV * (int)blockDim.x;
+  const Cut<kShift> cut = yr ? Cut<kShift>(yr, d, slots) : Cut<kShift>(hr, d, slots);
   Raw8<H> h[NV];
+  Raw8<T> y[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) h[i] = load_chunk((const H*)p.h + t * p.ldh, i, d, p.vec_h);
-  const Vector<T, NV, true> y(p.y ? (const T*)p.y + t * p.ldy : nullptr, d, p.vec_y);
-  const V gate(p.gate ? (const T*)p.gate + t * p.ldgate : nullptr, d, p.vec_gate);
-  const V post_weight(p.post_weight, d, p.vec_post_weight), post_bias(p.post_bias, d, p.vec_post_bias);
-  const V weight(p.weight, d, p.vec_weight), bias(p.bias, d, p.vec_bias);
-  norm_token<T, H, NV, true>(
-      p, t, red, [&](int i) { return h[i]; }, [&](int i) { return y.chunk(i); }, [&](int i) { return gate.chunk(i); },
+  for (int i = 0; i < NV; ++i) h[i] = load_chunk<kShift>(cut, hr, cut.start(i), d);
+  if (yr) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) y[i] = load_chunk<kShift>(cut, yr, cut.start(i), d);
+  }
+  const V gate(cut, gr, d);
+  const V post_weight(cut, p.post_weight, d), post_bias(cut, p.post_bias, d);
+  const V weight(cut, p.weight, d), bias(cut, p.bias, d);
+  norm_token<T, H, NV, kShift>(
+      cut, p, t, red, edge, [&](int i) { return h[i]; }, [&](int i) { return y[i]; }, [&](int i) { return gate.chunk(i); },
       post_weight, post_bias, weight, bias, [] {});
 }
 
 // ------------------------------------------------------- streaming kernels
-// Many tokens of wide, aligned rows: persistent blocks whose rows arrive in a
-// ring of shared-memory stages by bulk copies, the next rows' while this one
-// is worked on, so memory never waits for a statistic.
+// Many tokens of wide rows: persistent blocks whose rows arrive in a ring of
+// shared-memory stages by bulk copies, the next rows' while this one is worked
+// on, so memory never waits for a statistic.
 struct Ring {
   uint8_t* at;
   uint64_t* full;
@@ -358,26 +513,69 @@ struct Ring {
   }
 };
 
-template <typename T>
-__device__ __forceinline__ Raw8<T> read8(const void* row, int c) {
-  return load8((const T*)row + 8 * c, 8, true);
-}
+// One operand's rows on their way to a ring.  kShift: of any alignment.  A copy moves the whole 16-byte units that a row touches, so the
+// row stands in its stage at its own offset from such a boundary; units that
+// reach past the tensor's first or last element are not copied, patch() fills
+// in what those two rows then miss.
+template <typename T, bool kShift>
+struct Source {
+  const T* base;
+  int64_t ld, tokens;
+  int d;
+  __device__ __forceinline__ uint32_t room() const {  // of a row in a stage
+    return kShift ? ((uint32_t)(d * sizeof(T)) + 15 + 15) & ~15u : (uint32_t)(d * sizeof(T));
+  }
+  __device__ __forceinline__ uintptr_t row(int64_t t) const { return (uintptr_t)(base + t * ld); }
+  __device__ __forceinline__ const T* at(const uint8_t* stage, int64_t t) const {
+    return (const T*)(stage + (kShift ? row(t) & 15 : 0));
+  }
+  __device__ __forceinline__ void range(int64_t t, uintptr_t* from, uintptr_t* to) const {
+    *from = row(t);
+    *to = *from + d * sizeof(T);
+    if (!kShift) return;
+    const uintptr_t first = ((uintptr_t)base + 15) & ~(uintptr_t)15;
+    const uintptr_t last = (row(tokens - 1) + d * sizeof(T)) & ~(uintptr_t)15;
+    *from = max(*from & ~(uintptr_t)15, first);
+    *to = min((*to + 15) & ~(uintptr_t)15, last);
+  }
+  __device__ __forceinline__ uint32_t bytes(int64_t t) const {
+    uintptr_t from, to;
+    range(t, &from, &to);
+    return to > from ? (uint32_t)(to - from) : 0u;
+  }
+  __device__ __forceinline__ void fetch(uint8_t* stage, int64_t t, uint64_t* bar) const {
+    uintptr_t from, to;
+    range(t, &from, &to);
+    if (to > from) bulk_load(stage + (from - (row(t) & ~(uintptr_t)15)), (const void*)from, (uint32_t)(to - from), bar);
+  }
+  __device__ __forceinline__ void patch(uint8_t* stage, int64_t t) const {
+    uintptr_t from, to;
+    range(t, &from, &to);
+    T* const mine = const_cast<T*>(at(stage, t));
+    const int head = (int)(((int64_t)from - (int64_t)row(t)) / (int64_t)sizeof(T));  // elements before the copy
+    const int tail = (int)(((int64_t)to - (int64_t)row(t)) / (int64_t)sizeof(T));    // and its end
+    const int i = threadIdx.x;
+    if (i < head && i < d) mine[i] = base[t * ld + i];
+    if (tail + i < d && i < 16) mine[max(tail, 0) + i] = base[t * ld + max(tail, 0) + i];
+  }
+};
 
-template <typename T>
+template <typename T, bool kShift>
 __global__ void __launch_bounds__(1024) quantize_stream_kernel(const T* __restrict__ X, int64_t tokens, int d,
                                                                int64_t ldx, int8_t* __restrict__ q, int64_t ldq,
                                                                float* __restrict__ scale, int32_t* __restrict__ sum,
-                                                               int stages, uint32_t* status) {
+                                                               int stages, int stage_bytes, uint32_t* status) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t buf[64];
   __shared__ uint64_t full[kMaxStages];
   grid_launch_dependents();
-  const int chunks = d / 8;
-  const uint32_t bytes = (uint32_t)(d * sizeof(T));
-  Ring ring(smem, full, stages, (int)bytes, status);
+  const int step = 8 * (int)blockDim.x;
+  const Source<T, kShift> source = {X, ldx, tokens, d};
+  const Cut<kShift> cut(X + (int64_t)blockIdx.x * ldx, d, d + 7);
+  Ring ring(smem, full, stages, stage_bytes, status);
   auto fetch = [&](int64_t t, int s) {  // one thread
-    mbar_arrive_expect_tx(&full[s], bytes);
-    bulk_load(smem + (size_t)s * bytes, X + t * ldx, bytes, &full[s]);
+    mbar_arrive_expect_tx(&full[s], source.bytes(t));
+    source.fetch(smem + (size_t)s * stage_bytes, t, &full[s]);
   };
   if (threadIdx.x == 0)
     for (int s = 0; s < stages && blockIdx.x + (int64_t)s * gridDim.x < tokens; ++s)
@@ -385,21 +583,25 @@ __global__ void __launch_bounds__(1024) quantize_stream_kernel(const T* __restri
   RowReduce red(buf);
   for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
     ring.wait();
-    const uint8_t* row = ring.stage();
+    if (kShift && (t == 0 || t == tokens - 1)) {
+      source.patch(ring.stage(), t);
+      __syncthreads();
+    }
+    const T* row = source.at(ring.stage(), t);
     uint32_t top = 0;
 #pragma unroll 2
-    for (int c = threadIdx.x; c < chunks; c += blockDim.x) top = magnitude(read8<T>(row, c), top);
+    for (int e = cut.start(0); e < d; e += step) top = magnitude(load_chunk<kShift>(cut, row, e, d), top);
     const TokenScale ts(red.max_u32(magnitude_bits<T>(top)));
     int total = 0;
 #pragma unroll 2
-    for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
-      const Raw8<T> r = read8<T>(row, c);
+    for (int e = 8 * (int)threadIdx.x; e < d; e += step) {
+      const Raw8<T> r = kShift ? read_across(row, e, d) : load8(row + e, 8, true);
       Pair v[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) v[u] = get2(r, u);
       const uint2 w = ts.codes(v);
       total = __dp4a((int)w.x, 0x01010101, __dp4a((int)w.y, 0x01010101, total));
-      *reinterpret_cast<uint2*>(q + t * ldq + 8 * c) = w;
+      store_codes(q + t * ldq, e, d, w);
     }
     total = red.sum_s32(total);  // its barrier lies behind every read of the stage
     if (threadIdx.x == 0) {
@@ -418,44 +620,54 @@ __global__ void __launch_bounds__(1024) quantize_stream_kernel(const T* __restri
 // to come from L2 for every row, where here they stay in registers for all of
 // a block's rows (8192 rows of 4096 bf16 with both norms and a gate: 87, 68
 // and 76 us).
-template <typename T, typename H, int MaxThreads>
+template <typename T, typename H, bool kShift, int MaxThreads>
 __global__ void __launch_bounds__(MaxThreads, 1) norm_stream_kernel(const __grid_constant__ NormParams p) {
   constexpr int NV = kStreamChunks;
-  using V = Vector<T, NV, true>;
+  using V = Vector<T, NV, true, kShift>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t buf[64];
+  __shared__ uint64_t edge[kShift ? 32 * NV : 1];
   __shared__ uint64_t full[kMaxStages];
   const int d = p.d, stages = p.stages;
-  const uint32_t hb = (uint32_t)(d * sizeof(H)), tb = (uint32_t)(d * sizeof(T));
   const bool gates = p.gate && p.ldgate;  // a gate for each token comes with the row
-  const uint32_t bytes = hb + (p.y ? tb : 0u) + (gates ? tb : 0u);
+  const Source<H, kShift> h = {(const H*)p.h, p.ldh, p.tokens, d};
+  const Source<T, kShift> y = {(const T*)p.y, p.ldy, p.tokens, d}, g = {(const T*)p.gate, p.ldgate, p.tokens, d};
+  const uint32_t y_at = h.room(), g_at = y_at + (p.y ? y.room() : 0u);
   Ring ring(smem, full, stages, p.stage_bytes, p.status);
   auto fetch = [&](int64_t t, int s) {  // one thread
     uint8_t* at = smem + (size_t)s * p.stage_bytes;
-    mbar_arrive_expect_tx(&full[s], bytes);
-    bulk_load(at, (const H*)p.h + t * p.ldh, hb, &full[s]);
-    at += hb;
-    if (p.y) {
-      bulk_load(at, (const T*)p.y + t * p.ldy, tb, &full[s]);
-      at += tb;
-    }
-    if (gates) bulk_load(at, (const T*)p.gate + t * p.ldgate, tb, &full[s]);
+    mbar_arrive_expect_tx(&full[s], h.bytes(t) + (p.y ? y.bytes(t) : 0u) + (gates ? g.bytes(t) : 0u));
+    h.fetch(at, t, &full[s]);
+    if (p.y) y.fetch(at + y_at, t, &full[s]);
+    if (gates) g.fetch(at + g_at, t, &full[s]);
   };
   if (threadIdx.x == 0)
     for (int s = 0; s < stages && blockIdx.x + (int64_t)s * gridDim.x < p.tokens; ++s)
       fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
   RowReduce red(buf);
-  const V post_weight(p.post_weight, d, 1), weight(p.weight, d, 1), gate(gates ? nullptr : p.gate, d, 1);
-  const Vector<T, NV, false> post_bias(p.post_bias, d, 1), bias(p.bias, d, 1);  // no registers left for these
+  // the grid is a multiple of eight: all of a block's rows are aligned alike
+  const int64_t t0 = blockIdx.x;
+  const int slots = 8 * NV * (int)blockDim.x;
+  const Cut<kShift> cut = p.y ? Cut<kShift>((const T*)p.y + t0 * p.ldy, d, slots)
+                              : Cut<kShift>((const H*)p.h + t0 * p.ldh, d, slots);
+  const V post_weight(cut, p.post_weight, d), weight(cut, p.weight, d), gate(cut, gates ? nullptr : p.gate, d);
+  const Vector<T, NV, false, kShift> post_bias(cut, p.post_bias, d), bias(cut, p.bias, d);  // no registers left for these
   for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
     ring.wait();
-    const H* const h = (const H*)ring.stage();
-    const T* const y = (const T*)(h + d);
-    const T* const g = y + (p.y ? d : 0);
-    norm_token<T, H, NV, false>(
-        p, t, red, [&](int i) { return load_chunk(h, i, d, true); }, [&](int i) { return load_chunk(y, i, d, true); },
-        [&](int i) { return gates ? load_chunk(g, i, d, true) : gate.chunk(i); }, post_weight, post_bias, weight, bias,
-        [&] {
+    uint8_t* const stage = ring.stage();
+    if (kShift && (t == 0 || t == p.tokens - 1)) {
+      h.patch(stage, t);
+      if (p.y) y.patch(stage + y_at, t);
+      if (gates) g.patch(stage + g_at, t);
+      __syncthreads();
+    }
+    const H* const hr = h.at(stage, t);
+    const T *const yr = y.at(stage + y_at, t), *const gr = g.at(stage + g_at, t);
+    norm_token<T, H, NV, kShift>(
+        cut, p, t, red, edge, [&](int i) { return load_chunk<kShift>(cut, hr, cut.start(i), d); },
+        [&](int i) { return load_chunk<kShift>(cut, yr, cut.start(i), d); },
+        [&](int i) { return gates ? load_chunk<kShift>(cut, gr, cut.start(i), d) : gate.chunk(i); }, post_weight, post_bias, weight,
+        bias, [&] {
           // the barrier of the pre-norm's statistic lies behind every read
           const int64_t next = t + (int64_t)stages * gridDim.x;
           if (threadIdx.x == 0 && next < p.tokens) fetch(next, ring.s);
@@ -510,25 +722,34 @@ __global__ void __launch_bounds__(256) layout_int8_kernel(const uint32_t* __rest
 // block.
 dim3 row_block(int d, int nv) {
   const int lanes = (d + 8 * nv - 1) / (8 * nv);
-  return lanes <= 32 ? dim3(32, 4) : dim3((unsigned)((lanes + 31) / 32 * 32), 1);
+  return lanes <= 32 ? dim3(32, 4) : dim3((unsigned)std::min(1024, (lanes + 31) / 32 * 32), 1);
 }
 
 // Chunks a thread for rows straight to registers.  A few rows are a matter of
 // latency: the fewest chunks with which 1024 threads hold one.  Many are a
-// matter of instructions and bytes in flight: four, in whole warps up to 1024
-// elements.
+// matter of instructions: two, beside which a row's reductions and addresses
+// count for less, up to 16384 elements.
 int row_chunks(int d, int64_t tokens, int sms) {
-  if (tokens > 4 * sms) return d <= 256 ? 1 : d <= 512 ? 2 : 4;
-  return d <= 1024 * 8 ? 1 : d <= 1024 * 16 ? 2 : 4;
+  if (d > 1024 * 16) return 4;
+  return tokens > 4 * sms ? (d <= 256 ? 1 : 2) : (d <= 1024 * 8 ? 1 : 2);
 }
 
-// Whether the streaming kernel takes the call: rows a block wide whose bytes
-// bulk copies can move (16-byte addresses and sizes; a vector's loads too),
-// and enough of them to fill every block's ring more than once.
-bool streams(const NormParams& p, int sms) {
-  return p.weight && p.d >= kStreamMin && p.d <= 1024 * 8 * kStreamChunks && p.d % 8 == 0 && p.tokens > 4 * sms && p.vec_h && (!p.y || p.vec_y) &&
-         (!p.gate || p.vec_gate) && p.vec_weight && (!p.bias || p.vec_bias) && (!p.post_weight || p.vec_post_weight) &&
-         (!p.post_bias || p.vec_post_bias) && (!p.h_out || p.vec_h_out) && (!p.x || p.vec_x);
+// Whether a streaming kernel takes the call: rows a block wide, and enough of
+// them to fill every block's ring more than once.
+bool streams(int d, int64_t tokens, int sms) { return d >= kStreamMin && tokens > 4 * sms; }
+
+// Bytes of a row in a stage (Source::room).
+int row_room(int d, size_t size, bool shift) {
+  const int bytes = d * (int)size;
+  return shift ? (bytes + 30) & ~15 : bytes;
+}
+// Elements that a thread count has to cover: shifted cuts start up to seven early.
+int span(int d, bool shift) { return shift ? d + 7 : d; }
+// A streaming kernel's grid; its blocks' rows are aligned alike (Cut) when it
+// is a multiple of eight.
+unsigned stream_grid(int64_t tokens, int blocks, bool shift) {
+  const unsigned grid = (unsigned)std::min<int64_t>(tokens, (int64_t)blocks * device_info().sms);
+  return shift ? grid & ~7u : grid;
 }
 
 // The streaming kernels' blocks: threads for `each` elements of a row of d,
@@ -553,49 +774,59 @@ cudaError_t launch_quantize(const T* X, int64_t tokens, int d, int64_t ldx, int8
                             int32_t* sum, cudaStream_t st) {
   const bool vec = (uintptr_t)X % 16 == 0 && (ldx * (int64_t)sizeof(T)) % 16 == 0;
   const int sms = device_info().sms;
-  if (d >= kStreamMin && d % 8 == 0 && tokens > 4 * sms && vec) {
-    const StreamShape shape(d, 32, 32, d * (int)sizeof(T));
+  if (streams(d, tokens, sms)) {
+    const bool whole = vec && d % 8 == 0;
+    const int stage_bytes = (int)round_up(row_room(d, sizeof(T), !whole), 128);
+    const StreamShape shape(span(d, !whole), 32, 32, stage_bytes);
     if (shape.stages) {
       uint32_t* status = nullptr;
+      const auto kernel = whole ? quantize_stream_kernel<T, false> : quantize_stream_kernel<T, true>;
       cudaError_t e = int8_status_word(&status);
-      const int smem = shape.stages * d * (int)sizeof(T);
-      if (e == cudaSuccess) e = ensure_smem_limit((const void*)quantize_stream_kernel<T>, smem);
+      const int smem = shape.stages * stage_bytes;
+      if (e == cudaSuccess) e = ensure_smem_limit((const void*)kernel, smem);
       if (e != cudaSuccess) return e;
-      const unsigned grid = (unsigned)std::min<int64_t>(tokens, (int64_t)shape.blocks * sms);
-      quantize_stream_kernel<T><<<grid, shape.threads, smem, st>>>(X, tokens, d, ldx, q, ldq, scale, sum, shape.stages,
-                                                                    status);
+      const unsigned grid = stream_grid(tokens, shape.blocks, !whole);
+      kernel<<<grid, shape.threads, smem, st>>>(X, tokens, d, ldx, q, ldq, scale, sum, shape.stages, stage_bytes,
+                                                status);
       note_launch();
       return cudaGetLastError();
     }
   }
-  const int nv = row_chunks(d, tokens, sms);
-  const dim3 block = row_block(d, nv);
+  const int nv = row_chunks(span(d, !vec), tokens, sms);
+  const dim3 block = row_block(span(d, !vec), nv);
   const unsigned grid = (unsigned)((tokens + block.y - 1) / block.y);
+  auto launch = [&](auto whole, auto strided) {
+    (vec ? whole : strided)<<<grid, block, 0, st>>>(X, tokens, d, ldx, q, ldq, scale, sum);
+  };
   if (nv == 1)
-    quantize_tokens_kernel<T, 1><<<grid, block, 0, st>>>(X, tokens, d, ldx, q, ldq, scale, sum, vec);
+    launch(quantize_tokens_kernel<T, 1, false>, quantize_tokens_kernel<T, 1, true>);
   else if (nv == 2)
-    quantize_tokens_kernel<T, 2><<<grid, block, 0, st>>>(X, tokens, d, ldx, q, ldq, scale, sum, vec);
+    launch(quantize_tokens_kernel<T, 2, false>, quantize_tokens_kernel<T, 2, true>);
   else
-    quantize_tokens_kernel<T, 4><<<grid, block, 0, st>>>(X, tokens, d, ldx, q, ldq, scale, sum, vec);
+    launch(quantize_tokens_kernel<T, 4, false>, quantize_tokens_kernel<T, 4, true>);
   note_launch();
   return cudaGetLastError();
 }
 
-template <typename T, typename H, int MaxThreads>
+template <typename T, typename H, bool kShift, int MaxThreads>
 cudaError_t launch_stream(const NormParams& p, const StreamShape& shape, cudaStream_t st) {
   const int smem = p.stages * p.stage_bytes;
-  const cudaError_t e = ensure_smem_limit((const void*)norm_stream_kernel<T, H, MaxThreads>, smem);
+  const auto kernel = norm_stream_kernel<T, H, kShift, MaxThreads>;
+  const cudaError_t e = ensure_smem_limit((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)std::min<int64_t>(p.tokens, (int64_t)shape.blocks * device_info().sms);
-  norm_stream_kernel<T, H, MaxThreads><<<grid, shape.threads, smem, st>>>(p);
+  kernel<<<stream_grid(p.tokens, shape.blocks, kShift), shape.threads, smem, st>>>(p);
   note_launch();
   return cudaGetLastError();
 }
 
 template <typename T, typename H, int NV>
 cudaError_t launch_rows(const NormParams& p, cudaStream_t st) {
-  const dim3 block = row_block(p.d, NV);
-  norm_tokens_kernel<T, H, NV><<<(unsigned)((p.tokens + block.y - 1) / block.y), block, 0, st>>>(p);
+  const dim3 block = row_block(span(p.d, !p.aligned), NV);
+  const unsigned grid = (unsigned)((p.tokens + block.y - 1) / block.y);
+  if (p.aligned)
+    norm_tokens_kernel<T, H, NV, false><<<grid, block, 0, st>>>(p);
+  else
+    norm_tokens_kernel<T, H, NV, true><<<grid, block, 0, st>>>(p);
   note_launch();
   return cudaGetLastError();
 }
@@ -603,22 +834,28 @@ cudaError_t launch_rows(const NormParams& p, cudaStream_t st) {
 template <typename T, typename H>
 cudaError_t launch_norm(NormParams& p, cudaStream_t st) {
   const int sms = device_info().sms;
-  if (streams(p, sms)) {
-    p.stage_bytes = (int)round_up(p.d * (int)(sizeof(H) + (p.y ? sizeof(T) : 0) + (p.gate && p.ldgate ? sizeof(T) : 0)),
+  const bool whole = p.aligned && p.d % 8 == 0;
+  if (p.weight && span(p.d, !whole) <= 1024 * 8 * kStreamChunks && streams(p.d, p.tokens, sms)) {
+    p.stage_bytes = (int)round_up(row_room(p.d, sizeof(H), !whole) +
+                                      ((p.y ? 1 : 0) + (p.gate && p.ldgate ? 1 : 0)) * row_room(p.d, sizeof(T), !whole),
                                   128);
-    const StreamShape shape(p.d, 8 * kStreamChunks, 24, p.stage_bytes);
+    const StreamShape shape(span(p.d, !whole), 8 * kStreamChunks, 24, p.stage_bytes);
     p.stages = shape.stages;
     // 768 threads leave each 85 registers, which the vectors need; wider rows
     // have to do with 64
+    if (p.stages && whole)
+      return shape.threads <= 768 ? launch_stream<T, H, false, 768>(p, shape, st)
+                                  : launch_stream<T, H, false, 1024>(p, shape, st);
     if (p.stages)
-      return shape.threads <= 768 ? launch_stream<T, H, 768>(p, shape, st) : launch_stream<T, H, 1024>(p, shape, st);
+      return shape.threads <= 768 ? launch_stream<T, H, true, 768>(p, shape, st)
+                                  : launch_stream<T, H, true, 1024>(p, shape, st);
   }
-  const int nv = row_chunks(p.d, p.tokens, sms);
+  const int nv = row_chunks(span(p.d, !p.aligned), p.tokens, sms);
   return nv == 1 ? launch_rows<T, H, 1>(p, st) : nv == 2 ? launch_rows<T, H, 2>(p, st) : launch_rows<T, H, 4>(p, st);
 }
 
-int aligned_rows(const void* p, int64_t ld, gptq_dtype_t t) {
-  return (uintptr_t)p % 16 == 0 && (ld * (t == GPTQ_F32 ? 4 : 2)) % 16 == 0;
+bool aligned_rows(const void* p, int64_t ld, gptq_dtype_t t) {  // NULL: it is not read
+  return !p || (uintptr_t)p % 16 == 0 && (ld * (t == GPTQ_F32 ? 4 : 2)) % 16 == 0;
 }
 
 }  // namespace
@@ -673,15 +910,11 @@ gptq_status_t norm_tokens(const gptq_norm_t* a, cudaStream_t st) {
   p.beta = a->beta;
   p.eps = a->eps;
   p.layer = a->kind == GPTQ_NORM_LAYER;
-  p.vec_h = aligned_rows(a->h, a->ldh, a->ht);
-  p.vec_y = aligned_rows(a->y, a->ldy, a->yt);
-  p.vec_post_weight = aligned_rows(a->post_weight, 0, a->yt);
-  p.vec_post_bias = aligned_rows(a->post_bias, 0, a->yt);
-  p.vec_gate = aligned_rows(a->gate, a->ldgate, a->yt);
-  p.vec_weight = aligned_rows(a->weight, 0, a->yt);
-  p.vec_bias = aligned_rows(a->bias, 0, a->yt);
-  p.vec_h_out = aligned_rows(a->h_out, a->ldh_out, a->ht);
-  p.vec_x = aligned_rows(a->x, a->ldx, a->yt);
+  p.aligned = aligned_rows(a->h, a->ldh, a->ht) && aligned_rows(a->y, a->ldy, a->yt) &&
+              aligned_rows(a->post_weight, 0, a->yt) && aligned_rows(a->post_bias, 0, a->yt) &&
+              aligned_rows(a->gate, a->ldgate, a->yt) && aligned_rows(a->weight, 0, a->yt) &&
+              aligned_rows(a->bias, 0, a->yt) && aligned_rows(a->h_out, a->ldh_out, a->ht) &&
+              aligned_rows(a->x, a->ldx, a->yt);
   if (a->yt == GPTQ_F16)
     CUDA_TRY((a->ht == GPTQ_F32 ? launch_norm<__half, float>(p, st) : launch_norm<__half, __half>(p, st)));
   else if (a->yt == GPTQ_BF16)

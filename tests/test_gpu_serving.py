@@ -45,7 +45,8 @@ def _untouched(buf, rows, cols, fill=7.0):
     (1001, 77, BF16, 0), (6, 32767, F16, 0),
     # many rows: the streaming kernel, its ring going round, and what it leaves to the other
     (3001, 1024, BF16, 8), (1500, 4096, F32, 4), (2000, 11008, F16, 0), (700, 32768, F32, 0), (900, 1032, F16, 1),
-    (40000, 512, BF16, 0),
+    (40000, 512, BF16, 0), (1300, 1025, F16, 0), (700, 4001, BF16, 0), (601, 11007, F32, 0), (800, 2000, BF16, 3),
+    (3, 32768, F16, 3), (3, 16383, BF16, 0), (2500, 509, F16, 0), (2500, 254, BF16, 1), (900, 32765, F16, 0),
 ])
 def test_quantize_tokens_is_the_definition(lib, tokens, d, dtype, pad):
     x = _values(_rng(1, tokens, d), tokens, d, dtype)
@@ -214,7 +215,12 @@ NORMS = [  # tokens, d, type, residual type, kind, post, gate, alpha, beta, pad
     (1500, 512, BF16, BF16, "rms", True, "channel", 1.0, 0.5, 0), (5000, 264, F16, F32, "layer", True, "token", 1, 1, 8),
     (1203, 11008, F16, F32, "layer", True, "token", 0.7, 1.0, 0), (700, 16384, BF16, BF16, "rms", False, None, 1, 1, 0),
     (601, 32768, BF16, F32, "rms", True, "channel", 1, 1, 0), (999, 4096, F32, F32, "rms", True, "token", 1, 1, 0),
-    (2000, 4100, BF16, BF16, "rms", True, "channel", 1, 1, 0),
+    (2000, 4100, BF16, BF16, "rms", True, "channel", 1, 1, 0), (700, 4001, BF16, BF16, "layer", True, "token", 1, 1, 0),
+    (601, 11007, F16, F32, "rms", True, "channel", 0.7, 1, 0), (650, 1031, F32, F32, "layer", False, "token", 1, 1, 1),
+    (600, 16383, BF16, F32, "rms", False, None, 1, 1, 0), (3, 32768, BF16, F32, "rms", True, "token", 1, 1, 3),
+    (3, 16380, F16, F16, "layer", True, None, 1, 1, 1), (4, 8190, F16, F16, "rms", True, "channel", 1, 1, 1),
+    (2500, 249, BF16, BF16, "rms", True, "channel", 1, 1, 0), (2500, 511, F16, F32, "layer", True, "token", 1, 1, 0),
+ (640, 2056, F16, F16, "rms", True, "token", 1, 1, 5),
     (1001, 300, F16, F32, "rms", True, "channel", 1.0, 1.0, 1), (3, 32767, F16, F16, "rms", False, "token", 0.0, 1.0, 0),
 ]
 
@@ -261,6 +267,47 @@ def test_norm_first_block_and_in_place(lib):
     c = a.clone()
     got, gx = lib.norm_tokens(c, b, w, inplace=True)
     assert got is c and torch.equal(got, want) and torch.equal(gx, wx)
+
+
+@pytest.mark.parametrize("tokens,d,offset", [(7, 333, 1), (5, 40, 3), (700, 1024, 1), (601, 4001, 5), (650, 2051, 7)])
+@pytest.mark.parametrize("dtype", [F16, F32])
+def test_rows_that_start_anywhere(lib, tokens, d, offset, dtype):
+    """Tensors that begin and end inside a 16-byte unit, their surroundings
+    NaN, and outputs that do: first and last rows whole, nothing else written.
+    In place as well."""
+    rng = _rng(20, tokens, d)
+
+    def inside(t=None):
+        buf = torch.full((tokens * d + 32,), float("nan"), dtype=dtype, device="cuda")
+        view = buf[offset:offset + tokens * d].view(tokens, d)
+        if t is not None:
+            view.copy_(t)
+        return buf, view
+
+    h, y = _values(rng, tokens, d, dtype), _values(rng, tokens, d, dtype)
+    w = _values(rng, 1, d, dtype, 0.1)[0]
+    f = lambda t: t.double().numpy()  # noqa: E731
+    wh, dh, wx, dx = R.norm(f(h), f(y), f(w), None, f(w), None, None, 1, 1, "rms", float(np.float32(1e-6)))
+    (_, hv), (_, yv), (hb, ho), (xb, xo) = inside(h), inside(y), inside(), inside()
+    wbuf = torch.full((d + 16,), float("nan"), dtype=dtype, device="cuda")
+    wv = wbuf[offset:offset + d]
+    wv.copy_(w)
+    lib.gptq_norm_tokens(hv, yv, wv, post_weight=wv, h_out=ho, x=xo)
+    _within(ho, wh, dh * 1.01 + R.U[dtype] * np.abs(wh) * 1.01 + R.FLOOR[dtype], "h")
+    _within(xo, wx, dx * 1.01 + R.U[dtype] * np.abs(wx) * 1.01 + R.FLOOR[dtype], "x")
+    for b in (hb, xb):
+        assert bool(torch.isnan(b[:offset]).all()) and bool(torch.isnan(b[offset + tokens * d:]).all())
+    want, x1 = ho.clone(), xo.clone()
+    lib.gptq_norm_tokens(hv, yv, wv, post_weight=wv, h_out=hv, x=xo)
+    assert torch.equal(hv, want) and torch.equal(xo, x1)
+    t = lib.quantize_tokens(yv)
+    q, scale = R.quantize(y.float().numpy())
+    assert np.array_equal(t.q.cpu().numpy(), q) and np.array_equal(t.scale.cpu().numpy(), scale)
+    assert np.array_equal(t.sum.cpu().numpy(), q.sum(1, dtype=np.int64))
+    layer = R.random_layer(rng, 40, d)
+    p = R.product(q, scale, layer)
+    _within(lib.linear_int8(yv, R.on_device(lib, layer), dtype=F32), p, R.linear_tol(p, None, F32))
+    lib.gptq_int8_status()
 
 
 def test_norm_all_outputs_at_once(lib):
