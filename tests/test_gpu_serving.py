@@ -93,6 +93,8 @@ SIZES = [  # tokens, in, out
     (8, 4096, 129), (15, 777, 64), (16, 128, 4096), (17, 256, 1), (31, 3000, 513), (64, 4096, 1030), (100, 2000, 2731),
     (127, 127, 127), (128, 1024, 256), (129, 640, 384), (200, 4096, 255), (300, 100, 900), (513, 2048, 2049),
     (1000, 300, 520), (2050, 1152, 1024), (7, 32768, 40), (300, 32767, 130),
+    (20, 1, 40), (600, 5, 300), (2, 17, 3), (1, 12288, 300), (2, 12287, 149), (2, 12289, 33), (1, 32768, 9), (1, 15, 1000),
+    (2, 15, 149), (400, 8192, 2048), (130, 4096, 1024), (3, 2000, 11008),
 ]
 
 
@@ -438,6 +440,64 @@ def test_captured_runs_replay_on_new_inputs(lib, tokens):
         for c, o in zip((a, b), outs):
             want = lib.mlp_int8(*c)
             assert all(torch.equal(x, y) for x, y in zip(o, want))
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    """No set-up that a capture forbids: in a process of its own."""
+    import subprocess
+    import sys
+    code = """
+import torch, post_weight_quantization_13_b200 as g
+x = torch.randn(20, 512, device='cuda', dtype=torch.bfloat16)
+w = torch.ones(512, device='cuda', dtype=torch.bfloat16)
+layer = (torch.randint(-127, 127, (256, 512), dtype=torch.int8, device='cuda'), torch.ones(256, device='cuda'))
+down = (torch.randint(-127, 127, (512, 256), dtype=torch.int8, device='cuda'), torch.ones(512, device='cuda'))
+run = lambda: g.mlp_int8(x, x, w, layer, layer, down)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    y = run()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(y, run()))
+"""
+    root = __import__("os").path.dirname(__import__("os").path.dirname(__import__("os").path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_calls_from_several_threads(lib):
+    """Host threads on streams of their own: the same bits, and each thread's
+    errors its own."""
+    import threading
+    cases = [_case(lib, t, s) for s, t in enumerate((1, 30, 300, 900))]
+    want = [lib.mlp_int8(*c) for c in cases]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(c, w):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    r = lib.mlp_int8(*c)
+                    try:
+                        lib.linear_int8(c[0][:1].expand(5, c[0].shape[1]), c[3])
+                        bad.append("no error")
+                    except lib.GptqError as e:
+                        if e.status != 1:
+                            bad.append(e)
+                torch.cuda.current_stream().synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(r, w)):
+                bad.append("bits")
+        except Exception as e:      # noqa: BLE001
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=cw) for cw in zip(cases, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
 
 
 def test_the_stream_argument_orders_the_work(lib):

@@ -128,6 +128,53 @@ def test_layout_int8_refuses(g, call, status):
     assert g.lib.gptq_layout_int8(None, None, 0, 64, 8, None, 64, None, None) == 0
 
 
+def _linear(g, w, X=A, xt=1, tokens=40, in_=64, ldx=64, out=32, bias=None, Y=A, yt=1, ldy=32, ws=1 << 20,
+            ws_bytes=1 << 20):
+    return g.lib.gptq_linear_int8(X, xt, tokens, in_, ldx, w, out, bias, Y, yt, ldy, ws, ws_bytes, None)
+
+
+def _linear_gated(g, w, u, X=A, xt=1, tokens=40, in_=64, ldx=64, out=32, act=0, Y=A, yt=1, ldy=32, ws=1 << 20,
+                  ws_bytes=1 << 20):
+    return g.lib.gptq_linear_int8_gated(X, xt, tokens, in_, ldx, w, u, out, act, Y, yt, ldy, ws, ws_bytes, None)
+
+
+WORKSPACE = 4
+
+
+@pytest.mark.parametrize("call,status", [
+    (dict(tokens=-1), INVALID), (dict(in_=0), INVALID), (dict(out=-1), INVALID), (dict(in_=32769), UNSUPPORTED),
+    (dict(xt=3), INVALID), (dict(yt=-1), INVALID), (dict(X=None), INVALID), (dict(X=A + 1), INVALID),
+    (dict(ldx=63), INVALID), (dict(Y=None), INVALID), (dict(ldy=31), INVALID), (dict(ws=None), WORKSPACE),
+    (dict(ws=A + 16), WORKSPACE), (dict(ws_bytes=64 * 40), WORKSPACE), (dict(ws_bytes=0), WORKSPACE),
+])
+def test_linear_int8_refuses(g, S, call, status):
+    assert _linear(g, _layer(S), **call) == status
+    assert g.gptq_last_error()
+    assert _linear_gated(g, _layer(S), _layer(S), **call) == status
+
+
+def test_linear_int8_other_arguments(g, S):
+    assert _linear(g, _layer(S, ldw=72)) == INVALID
+    assert _linear(g, _layer(S), bias=A + 1) == INVALID
+    assert _linear_gated(g, _layer(S), None) == INVALID
+    assert _linear_gated(g, _layer(S), _layer(S), act=-1) == INVALID
+    assert _linear(g, None, tokens=0, X=None, Y=None, ws=None, ws_bytes=0) == 0
+    assert _linear_gated(g, None, None, out=0, Y=None, ws=None, ws_bytes=0) == 0
+
+
+def test_linear_int8_workspace_sizes(g):
+    """Codes in 16-byte rows, a scale and a sum for each token; none where one
+    kernel does both; 0 for sizes no call takes."""
+    size = g.gptq_linear_int8_ws_bytes
+    assert size(1, 4096) == 0 and size(2, 4096) == 0
+    assert size(40, 65) >= 40 * (80 + 4 + 4) and size(3, 4096) >= 3 * (4096 + 8)
+    assert size(1 << 26, 32768) >= (1 << 26) * (32768 + 8)
+    assert size(-1, 64) == 0 and size(4, 0) == 0 and size(4, 32769) == 0 and size((1 << 26) + 1, 64) == 0
+    for t in (1, 3, 100, 5000):
+        for d in (1, 15, 4096, 32768):
+            assert size(t, d) % 256 == 0
+
+
 # ------------------------------------------------------------ Python functions
 def test_python_calls_refuse_cpu_tensors(g):
     x = torch.ones(4, 64)
@@ -173,6 +220,37 @@ def test_python_calls_check_types_and_shapes(g):
         g.norm_tokens(x, x)
     with pytest.raises(ValueError):
         g.norm_tokens(x, x.half(), w)
+
+
+def test_calls_into_given_tensors_check_types_and_shapes(g):
+    t = g.Int8Tokens(torch.zeros(4, 64, dtype=torch.int8), torch.ones(4), torch.zeros(4, dtype=torch.int32))
+    layer = g.Int8Layer(torch.zeros(8, 64, dtype=torch.int8), torch.ones(8))
+    x, Y = torch.ones(4, 64), torch.empty(4, 8)
+    for call in (lambda: g.gptq_matmul_int8(t, layer, torch.empty(4, 9)),
+                 lambda: g.gptq_matmul_int8(t, layer, Y, bias=torch.ones(9)),
+                 lambda: g.gptq_matmul_int8_gated(t, layer, layer, Y, act="no"),
+                 lambda: g.gptq_linear_int8(x[:, :63], layer, Y),
+                 lambda: g.gptq_linear_int8(x.t().contiguous().t(), layer, Y),
+                 lambda: g.gptq_linear_int8_gated(x, layer, layer._replace(scale=torch.ones(3)), Y),
+                 lambda: g.gptq_quantize_tokens(x, t.q, torch.ones(3), t.sum),
+                 lambda: g.gptq_quantize_tokens(x, t.q.int(), t.scale, t.sum),
+                 lambda: g.gptq_norm_tokens(x, x, torch.ones(64), x=torch.empty(4, 63)),
+                 lambda: g.gptq_norm_tokens(x, x, torch.ones(64), h_out=x.half()),
+                 lambda: g.gptq_norm_tokens(x, x, torch.ones(64), tokens=t._replace(scale=torch.ones(4).half())),
+                 lambda: g.gptq_layout_int8(torch.zeros(8, 16, dtype=torch.int32), torch.zeros(7, dtype=torch.int32), 8,
+                                            layer.weight),
+                 lambda: g.gptq_layout_int8(torch.zeros(8, 15, dtype=torch.int32), torch.zeros(8, dtype=torch.int32), 8,
+                                            layer.weight)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        g.linear_int8(x, [layer.weight])
+    with pytest.raises(TypeError):
+        g.linear_int8("x", layer)
+    with pytest.raises(TypeError):
+        g.linear_int8(x, layer, dtype="float32")
+    with pytest.raises(TypeError):
+        g.quantize_tokens(x.double())
 
 
 def test_int8_layer_needs_one_scale_per_channel(g):
