@@ -425,12 +425,13 @@ gptq_status_t gptq_quantize_layer_noalloc_status(void* stream);
  *   gptq_matmul_int8          tokens x layer^T
  *   gptq_matmul_int8_gated    act(tokens x gate^T) * (tokens x up^T)
  *   gptq_linear_int8(_gated)  the same from floating activations
- *   gptq_int8_status          device-side status of the two products
+ *   gptq_int8_status          device-side status of all of these
  *
  * All take 0 <= tokens <= 67108864 (2^26) and 1 <= in <= 32768 (here also
  * called d), work on the calling thread's current device, are asynchronous
  * on stream and keep no state between calls, so any number of them may
- * overlap on any streams and be captured into graphs.
+ * overlap on any streams and be captured into graphs.  Outputs overlap no
+ * input and no other output unless a call says otherwise.
  * tokens == 0 and out == 0 are no-ops.  Activations are [tokens][in], tokens
  * in rows (the transpose of the Hessian's X).
  */
@@ -576,7 +577,8 @@ gptq_status_t gptq_matmul_int8_gated(const gptq_int8_tokens_t* x,
  * tokens' codes live in the workspace ws of ws_bytes >=
  * gptq_linear_int8_ws_bytes(tokens, in), 256-byte aligned, which needs no
  * initialisation and must not be used by two calls at once; for a few tokens
- * that size is 0 (one kernel does both, ws may be NULL).
+ * that size is 0 (one kernel does both, ws may be NULL).  Y overlaps neither X
+ * nor ws.
  */
 size_t gptq_linear_int8_ws_bytes(int64_t tokens, int64_t in);
 
@@ -597,8 +599,8 @@ gptq_status_t gptq_linear_int8_gated(const void* X, gptq_dtype_t xt,
 
 /*
  * Waits for stream and returns GPTQ_ERR_TIMEOUT if a bounded device-side wait
- * in any int8 product on the current device has given up since the last such
- * call (the products concerned are incomplete), else GPTQ_OK.  Clears the
+ * in any of these calls on the current device has given up since the last such
+ * call (the results concerned are incomplete), else GPTQ_OK.  Clears the
  * status.
  */
 gptq_status_t gptq_int8_status(void* stream);

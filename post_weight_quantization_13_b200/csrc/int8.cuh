@@ -1,6 +1,6 @@
-// Device code shared by the 8-bit serving kernels (tokens.cu, int8_mm.cu):
-// typed element access, the token quantizer's arithmetic, the products'
-// epilogue.
+// Device code shared by the 8-bit serving kernels (tokens.cu, int8_mm.cu,
+// int8_pair.cu, int8_rows.cu): typed element access, the loops that feed the
+// tensor cores, the token quantizer's arithmetic, the products' epilogue.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -170,6 +170,7 @@ __device__ __forceinline__ uint32_t elect_lane() {
       : "=r"(leader));
   return leader;
 }
+// As mbar_wait, false once the limit is past.
 __device__ __forceinline__ bool wait_at(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -273,6 +274,14 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
+}
+
+// A block that gave up a wait lets the copies it has under way land before its
+// shared memory goes to another.
+__device__ __forceinline__ void let_copies_land() {
+  const uint64_t start = globaltimer();
+  while (globaltimer() - start < 1000000ull) {
+  }
 }
 
 // ------------------------------------------------------------ token quantizer

@@ -29,7 +29,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kGroups = 2;             // that take the batches in turn
 constexpr int kBatch = 8;              // weight rows of a reduction
 constexpr int kSlice = kThreads * 16;  // columns of one step
-constexpr int kMaxSteps = 3;           // in <= 12288: two batches of the widest rows fill the ring
+constexpr int kMaxSteps = 3;           // in <= 12288: two batches of the widest rows nearly fill the ring
 constexpr int kMaxSlots = 40;          // of the ring
 constexpr int kSmem = 227 * 1024 - 6 * 1024;  // dynamic shared memory; the rest is the static arrays'
 
@@ -197,10 +197,7 @@ __global__ void __launch_bounds__(kGroups * kThreads + 32, 1) int8_rows_kernel(c
     for (int c = 0; c < n_end - n_begin; c += group) {
       if (!wait_at(empty0 + 8 * slot, phase)) {
         raise_status(kp.status, ST_TIMEOUT);
-        // let the copies under way land before the block can end
-        const uint64_t start = globaltimer();
-        while (globaltimer() - start < 1000000ull) {
-        }
+        let_copies_land();
         break;
       }
       const int n = n_begin + c, rows = min(group, n_end - n);
@@ -370,6 +367,7 @@ __global__ void __launch_bounds__(kGroups * kThreads + 32, 1) int8_rows_kernel(c
         }
       }
     }
+    if (gave_up) let_copies_land();
   }
 }
 
@@ -388,7 +386,8 @@ cudaError_t launch(RowsParams& kp, cudaStream_t st, int sms) {
   kp.group = kBatch / G;
   while (kp.group > 1 && G * kp.group * kp.row_bytes > 32768) kp.group /= 2;
   kp.slot_bytes = (G * kp.group * kp.row_bytes + 127) / 128 * 128;
-  // at least two batches' (12288 wide, two tokens: 196 of the 198 KB left)
+  // at least the one batch that a group holds, and two (one a group) but for
+  // the widest rows with padding
   kp.slots = std::min(kMaxSlots, (kSmem - fixed) / kp.slot_bytes);
   const int smem = fixed + kp.slots * kp.slot_bytes;
   const void* f = (const void*)int8_rows_kernel<G, T>;

@@ -241,7 +241,9 @@ __device__ __forceinline__ void quantize_row(const Cut<kShift>& cut, const Pair 
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const bool inner = (threadIdx.x >> 5) + 1 < warps;
-      const uint64_t next = inner ? edge[32 * i + warp + 1] : i + 1 < NV ? edge[32 * (i + 1 < NV ? i + 1 : i) + warp + 1 - warps] : 0;
+      const uint64_t next = inner        ? edge[32 * i + warp + 1]
+                            : i + 1 < NV ? edge[32 * (i + 1 < NV ? i + 1 : i) + warp + 1 - warps]
+                                         : 0;
       const uint64_t eight = last[i] >> (8 * m) | next << (64 - 8 * m);
       const int e = cut.start(i) + m;
       if (e < d) store_codes(q, e, d, make_uint2((uint32_t)eight, (uint32_t)(eight >> 32)));
@@ -389,8 +391,9 @@ __device__ __forceinline__ void store_row(const Cut<kShift>& cut, T* __restrict_
 template <typename T, typename H, int NV, bool kShift, typename LoadH, typename LoadY, typename LoadGate, typename V,
           typename B, typename Release>
 __device__ __forceinline__ void norm_token(const Cut<kShift>& cut, const NormParams& p, int64_t t, RowReduce& red,
-                                           uint64_t (&edge)[kShift ? 32 * NV : 1], LoadH h, LoadY y, LoadGate gate, const V& post_weight, const B& post_bias, const V& weight,
-                                           const B& bias, Release release) {
+                                           uint64_t (&edge)[kShift ? 32 * NV : 1], LoadH h, LoadY y, LoadGate gate,
+                                           const V& post_weight, const B& post_bias, const V& weight, const B& bias,
+                                           Release release) {
   const int d = p.d;
   const Pair alpha(p.alpha);
   Pair v[NV][4];
@@ -446,8 +449,8 @@ __device__ __forceinline__ void norm_token(const Cut<kShift>& cut, const NormPar
   }
 }
 
-// A row a warp or a block, every operand straight to registers: few tokens,
-// narrow rows, unaligned rows.
+// A row a warp or a block, every operand straight to registers: few tokens or
+// narrow rows (one token of 4096 takes 2.3 us, all latency).
 template <typename T, typename H, int NV, bool kShift>
 __global__ void __launch_bounds__(1024) norm_tokens_kernel(const __grid_constant__ NormParams p) {
   __shared__ uint32_t buf[64];
@@ -481,7 +484,11 @@ __global__ void __launch_bounds__(1024) norm_tokens_kernel(const __grid_constant
 // ------------------------------------------------------- streaming kernels
 // Many tokens of wide rows: persistent blocks whose rows arrive in a ring of
 // shared-memory stages by bulk copies, the next rows' while this one is worked
-// on, so memory never waits for a statistic.
+// on, so memory never waits for a statistic.  Bound by memory where rows are
+// read and written in turn (8192 x 4096 bf16, both norms and a gate: 54 to 57 us
+// for 268 MB; more warps do not help), by its four reductions a row where rows
+// are so wide that one block fills an SM (1001 x 11008 layer norms: 44 us, the
+// bytes alone 24).
 struct Ring {
   uint8_t* at;
   uint64_t* full;
@@ -513,10 +520,11 @@ struct Ring {
   }
 };
 
-// One operand's rows on their way to a ring.  kShift: of any alignment.  A copy moves the whole 16-byte units that a row touches, so the
-// row stands in its stage at its own offset from such a boundary; units that
-// reach past the tensor's first or last element are not copied, patch() fills
-// in what those two rows then miss.
+// One operand's rows on their way to a ring.  kShift: of any alignment.  A copy
+// moves the whole 16-byte units that a row touches, so the row stands in its
+// stage at its own offset from such a boundary; units that reach past the
+// tensor's first or last element are not copied, patch() fills in what those
+// two rows then miss.
 template <typename T, bool kShift>
 struct Source {
   const T* base;
@@ -557,6 +565,7 @@ struct Source {
     const int i = threadIdx.x;
     if (i < head && i < d) mine[i] = base[t * ld + i];
     if (tail + i < d && i < 16) mine[max(tail, 0) + i] = base[t * ld + max(tail, 0) + i];
+    fence_proxy_async_smem();  // a copy writes here next
   }
 };
 
@@ -608,10 +617,11 @@ __global__ void __launch_bounds__(1024) quantize_stream_kernel(const T* __restri
       scale[t] = ts.scale;
       sum[t] = total;
       const int64_t next = t + (int64_t)stages * gridDim.x;
-      if (next < tokens) fetch(next, ring.s);
+      if (next < tokens && !ring.gave_up) fetch(next, ring.s);
     }
     ring.advance();
   }
+  if (ring.gave_up) let_copies_land();
 }
 
 // A thread has 16 elements of the row: with 8, what a row costs beside its
@@ -651,7 +661,7 @@ __global__ void __launch_bounds__(MaxThreads, 1) norm_stream_kernel(const __grid
   const Cut<kShift> cut = p.y ? Cut<kShift>((const T*)p.y + t0 * p.ldy, d, slots)
                               : Cut<kShift>((const H*)p.h + t0 * p.ldh, d, slots);
   const V post_weight(cut, p.post_weight, d), weight(cut, p.weight, d), gate(cut, gates ? nullptr : p.gate, d);
-  const Vector<T, NV, false, kShift> post_bias(cut, p.post_bias, d), bias(cut, p.bias, d);  // no registers left for these
+  const Vector<T, NV, false, kShift> post_bias(cut, p.post_bias, d), bias(cut, p.bias, d);  // no registers for these
   for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
     ring.wait();
     uint8_t* const stage = ring.stage();
@@ -666,14 +676,15 @@ __global__ void __launch_bounds__(MaxThreads, 1) norm_stream_kernel(const __grid
     norm_token<T, H, NV, kShift>(
         cut, p, t, red, edge, [&](int i) { return load_chunk<kShift>(cut, hr, cut.start(i), d); },
         [&](int i) { return load_chunk<kShift>(cut, yr, cut.start(i), d); },
-        [&](int i) { return gates ? load_chunk<kShift>(cut, gr, cut.start(i), d) : gate.chunk(i); }, post_weight, post_bias, weight,
-        bias, [&] {
+        [&](int i) { return gates ? load_chunk<kShift>(cut, gr, cut.start(i), d) : gate.chunk(i); }, post_weight,
+        post_bias, weight, bias, [&] {
           // the barrier of the pre-norm's statistic lies behind every read
           const int64_t next = t + (int64_t)stages * gridDim.x;
-          if (threadIdx.x == 0 && next < p.tokens) fetch(next, ring.s);
+          if (threadIdx.x == 0 && next < p.tokens && !ring.gave_up) fetch(next, ring.s);
         });
     ring.advance();
   }
+  if (ring.gave_up) let_copies_land();
 }
 
 // ------------------------------------------------------------ weight layout

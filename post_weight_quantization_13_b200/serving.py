@@ -12,7 +12,9 @@ tensors the caller owns.
     h, xq = norm_tokens(h, y, weight, quantize=True)
     h, y = mlp_int8(h, y, weight, gate, up, down)  # a decoder block's MLP half
 
-Activations are 2-D, tokens in rows, rows contiguous (any row stride).
+Activations are 2-D, tokens in rows, rows contiguous (any row stride).  These
+are inference calls: a solved layer is frozen, and no gradient flows through
+them.
 """
 from __future__ import annotations
 
@@ -184,7 +186,9 @@ def gptq_layout_int8(qweight, zeros, bits, weight, zero=None, stream=None) -> No
     if qweight.dtype not in (torch.int32, torch.uint32) or not qweight.is_contiguous() or \
             qweight.numel() != out * in_ * bits // 32 or qweight.device != dev:
         raise ValueError(f"qweight must hold {out} contiguous rows of {in_ * bits // 32} words on {dev}")
-    z = _vector(zeros.reshape(-1), out, torch.int32, dev, "zeros")
+    if not zeros.is_contiguous():
+        raise ValueError("zeros must be contiguous")
+    z = _vector(zeros.view(-1), out, torch.int32, dev, "zeros")
     z8 = None if zero is None else _vector(zero, out, torch.int32, dev, "zero")
     _call(dev, stream, lib.gptq_layout_int8, qweight.data_ptr(), z, out, in_, int(bits), weight.data_ptr(), ld, z8)
 
@@ -299,7 +303,7 @@ def _workspace(ws, dev):
 
 def gptq_int8_status(stream=None) -> None:
     """Wait for the stream and raise GptqError if a bounded device-side wait
-    of an int8 product on this device has given up since the last call."""
+    of any of these calls on this device has given up since the last time."""
     _check(lib.gptq_int8_status(_stream(stream)))
 
 

@@ -239,6 +239,8 @@ def test_calls_into_given_tensors_check_types_and_shapes(g):
                  lambda: g.gptq_norm_tokens(x, x, torch.ones(64), tokens=t._replace(scale=torch.ones(4).half())),
                  lambda: g.gptq_layout_int8(torch.zeros(8, 16, dtype=torch.int32), torch.zeros(7, dtype=torch.int32), 8,
                                             layer.weight),
+                 lambda: g.gptq_layout_int8(torch.zeros(8, 16, dtype=torch.int32),
+                                            torch.zeros(16, dtype=torch.int32)[::2], 8, layer.weight),
                  lambda: g.gptq_layout_int8(torch.zeros(8, 15, dtype=torch.int32), torch.zeros(8, dtype=torch.int32), 8,
                                             layer.weight)):
         with pytest.raises(ValueError):
