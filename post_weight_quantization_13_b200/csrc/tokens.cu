@@ -293,6 +293,7 @@ struct NormParams {
   float alpha, beta, eps;
   int layer;
   int stages, stage_bytes;  // of the streaming kernel
+  int post_bias_at, bias_at;  // their places in its shared memory, 0: none
   uint32_t* status;
   int aligned;  // every operand's rows start on 16-byte boundaries
 };
@@ -316,6 +317,25 @@ struct Vector {
   __device__ __forceinline__ Raw8<T> chunk(int i) const {
     return kEarly ? r[kEarly ? i : 0] : load_vector<kShift>(cut, p, cut.start(i), d);
   }
+};
+
+// A norm's bias in the streaming kernel, where the registers are full: in shared
+// memory, each thread's chunks written and read by itself; where there is no
+// room (at null), fetched when it is used.  (Two layer norms a row: 4096 x 8192
+// 112 us with both biases from L2 for every row, 92 from here; 8192 x 4096 84
+// and 78.)
+template <typename T, int NV, bool kShift>
+struct SharedVector {
+  Vector<T, NV, false, kShift> from;
+  Raw8<T>* at;  // the thread's first chunk
+  __device__ __forceinline__ SharedVector(const Cut<kShift>& cut, const void* p, int d, uint8_t* smem, int offset)
+      : from(cut, p, d), at(p && offset ? (Raw8<T>*)(smem + offset) + threadIdx.x : nullptr) {
+    if (at)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) at[i * blockDim.x] = from.chunk(i);
+  }
+  __device__ __forceinline__ explicit operator bool() const { return (bool)from; }
+  __device__ __forceinline__ Raw8<T> chunk(int i) const { return at ? at[i * blockDim.x] : from.chunk(i); }
 };
 
 // Zero outside the row, so that nothing there reaches a statistic.
@@ -487,7 +507,7 @@ __global__ void __launch_bounds__(1024) norm_tokens_kernel(const __grid_constant
 // on, so memory never waits for a statistic.  Bound by memory where rows are
 // read and written in turn (8192 x 4096 bf16, both norms and a gate: 54 to 57 us
 // for 268 MB; more warps do not help), by its four reductions a row where rows
-// are so wide that one block fills an SM (1001 x 11008 layer norms: 44 us, the
+// are so wide that one block fills an SM (1001 x 11008 layer norms: 43 us, the
 // bytes alone 24).
 struct Ring {
   uint8_t* at;
@@ -661,7 +681,8 @@ __global__ void __launch_bounds__(MaxThreads, 1) norm_stream_kernel(const __grid
   const Cut<kShift> cut = p.y ? Cut<kShift>((const T*)p.y + t0 * p.ldy, d, slots)
                               : Cut<kShift>((const H*)p.h + t0 * p.ldh, d, slots);
   const V post_weight(cut, p.post_weight, d), weight(cut, p.weight, d), gate(cut, gates ? nullptr : p.gate, d);
-  const Vector<T, NV, false, kShift> post_bias(cut, p.post_bias, d), bias(cut, p.bias, d);  // no registers for these
+  const SharedVector<T, NV, kShift> post_bias(cut, p.post_bias, d, smem, p.post_bias_at),
+      bias(cut, p.bias, d, smem, p.bias_at);
   for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
     ring.wait();
     uint8_t* const stage = ring.stage();
@@ -768,11 +789,11 @@ unsigned stream_grid(int64_t tokens, int blocks, bool shift) {
 // (0: not two).
 struct StreamShape {
   int threads, blocks, stages;
-  StreamShape(int d, int each, int warps, int stage_bytes) {
+  StreamShape(int d, int each, int warps, int stage_bytes, int fixed_bytes = 0) {
     threads = std::min(1024, ((d + each - 1) / each + 31) / 32 * 32);
     blocks = std::max(1, warps * 32 / threads);
     for (;; --blocks) {  // fewer blocks where their rings do not fit
-      stages = std::min(kMaxStages, (kSmemPerSm / blocks - 2048) / stage_bytes);
+      stages = std::min(kMaxStages, (kSmemPerSm / blocks - 2048 - fixed_bytes) / stage_bytes);
       if (stages >= 2) break;
       stages = 0;
       if (blocks == 1) break;
@@ -820,8 +841,8 @@ cudaError_t launch_quantize(const T* X, int64_t tokens, int d, int64_t ldx, int8
 }
 
 template <typename T, typename H, bool kShift, int MaxThreads>
-cudaError_t launch_stream(const NormParams& p, const StreamShape& shape, cudaStream_t st) {
-  const int smem = p.stages * p.stage_bytes;
+cudaError_t launch_stream(const NormParams& p, const StreamShape& shape, int bias_bytes, cudaStream_t st) {
+  const int smem = p.stages * p.stage_bytes + bias_bytes;
   const auto kernel = norm_stream_kernel<T, H, kShift, MaxThreads>;
   const cudaError_t e = ensure_smem_limit((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
@@ -850,16 +871,28 @@ cudaError_t launch_norm(NormParams& p, cudaStream_t st) {
     p.stage_bytes = (int)round_up(row_room(p.d, sizeof(H), !whole) +
                                       ((p.y ? 1 : 0) + (p.gate && p.ldgate ? 1 : 0)) * row_room(p.d, sizeof(T), !whole),
                                   128);
-    const StreamShape shape(span(p.d, !whole), 8 * kStreamChunks, 24, p.stage_bytes);
+    const int width = span(p.d, !whole);
+    StreamShape shape(width, 8 * kStreamChunks, 24, p.stage_bytes);
+    const int vector = shape.threads * kStreamChunks * 8 * (int)sizeof(T), biases = (p.post_bias ? 1 : 0) + (p.bias ? 1 : 0);
+    int bias_bytes = 0;
+    if (biases) {
+      const StreamShape with(width, 8 * kStreamChunks, 24, p.stage_bytes, biases * vector);
+      if (with.stages && with.blocks == shape.blocks) {
+        shape = with;
+        bias_bytes = biases * vector;
+        p.post_bias_at = p.post_bias ? shape.stages * p.stage_bytes : 0;
+        p.bias_at = p.bias ? shape.stages * p.stage_bytes + bias_bytes - vector : 0;
+      }
+    }
     p.stages = shape.stages;
     // 768 threads leave each 85 registers, which the vectors need; wider rows
     // have to do with 64
     if (p.stages && whole)
-      return shape.threads <= 768 ? launch_stream<T, H, false, 768>(p, shape, st)
-                                  : launch_stream<T, H, false, 1024>(p, shape, st);
+      return shape.threads <= 768 ? launch_stream<T, H, false, 768>(p, shape, bias_bytes, st)
+                                  : launch_stream<T, H, false, 1024>(p, shape, bias_bytes, st);
     if (p.stages)
-      return shape.threads <= 768 ? launch_stream<T, H, true, 768>(p, shape, st)
-                                  : launch_stream<T, H, true, 1024>(p, shape, st);
+      return shape.threads <= 768 ? launch_stream<T, H, true, 768>(p, shape, bias_bytes, st)
+                                  : launch_stream<T, H, true, 1024>(p, shape, bias_bytes, st);
   }
   const int nv = row_chunks(span(p.d, !p.aligned), p.tokens, sms);
   return nv == 1 ? launch_rows<T, H, 1>(p, st) : nv == 2 ? launch_rows<T, H, 2>(p, st) : launch_rows<T, H, 4>(p, st);
