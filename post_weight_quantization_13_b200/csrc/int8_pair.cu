@@ -14,8 +14,9 @@
 //   warp 0     TMA producer: its own operand halves; the transactions of both
 //              CTAs are counted on the first CTA's barrier
 //   warp 1     (in the first CTA) issues the pair's MMAs and commits them to both
-//   warps 2-9  epilogue: scales, bias or activation, and 64-byte row pieces
-//              through shared memory to coalesced stores.  Two warps share a
+//   warps 2-9  epilogue: scales, bias or activation, then whole sectors of a
+//              row from each thread, or 64-byte row pieces through shared
+//              memory to coalesced stores.  Two warps share a
 //              quarter of tensor memory and halve its columns between them:
 //              the last tile's epilogue has nothing to hide under, and with
 //              four warps it took 4.9 of the 19 us of a product of one tile
@@ -53,7 +54,7 @@ struct PairParams {
   const float* bias;
   void* Y;
   int64_t ldy;
-  int tokens, out, act, vec;
+  int tokens, out, act, vec, vec32;
   int ktiles, bn, stages, stage_bytes;
   int mtiles, ntiles, tiles, pairs;
   uint32_t* status;
@@ -114,6 +115,13 @@ __device__ __forceinline__ void scale_columns(const float (&v)[N], Pair (&y)[N /
     y[i / 2] = mul2(mul2(Pair((float)a[0], (float)a[1]), t), Pair(s.x, s.y));
     y[i / 2 + 1] = mul2(mul2(Pair((float)a[2], (float)a[3]), t), Pair(s.z, s.w));
   }
+}
+
+// Eight 32-bit words to a 32-byte boundary.
+__device__ __forceinline__ void store_sector(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 template <int G, typename T>
@@ -245,7 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------ epilogue
     constexpr int CW = 64 / (int)sizeof(T);  // columns of a 64-byte row piece
-    constexpr int STEP = CW < 16 ? CW : 16;  // columns of a step, see below
+    constexpr int STEP = 16;                 // columns of a step, see below
     const int quarter = warp & 3, e = threadIdx.x - 64;
     const int bn = kp.bn, width = G == 2 ? half : bn;  // channels of the tile's output
     const int c_begin = (warp - 2) / 4 * (width / 2), c_end = c_begin + width / 2;  // this warp's
@@ -286,6 +294,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       T* const rows = (T*)kp.Y + (int64_t)(t - lane) * kp.ldy;
       const int live = min(32, kp.tokens - (t - lane));  // rows of this warp inside the result
       for (int c0 = c_begin; c0 < c_end; c0 += CW) {
+        // Rows on 32-byte boundaries are written by whole sectors without the
+        // way through shared memory (4096 x 4096, k 1024: 24.7 us, so 23.2;
+        // the gated form, short of instruction cache, 40.4 and 43.1).
+        const bool direct = G == 1 && kp.vec32 && n0 + c0 + CW <= kp.out;
         // sixteen columns a step, not unrolled further: the loop has to stay
         // in the instruction cache (unrolled over 64 columns, the gated form
         // waited for instructions most of the time and took 1.4 times as long)
@@ -329,6 +341,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const float v[2] = {f.x, f.y};
             round_n<2>(v, o + 2 * i);
           }
+          if (direct) {
+            if (lane < live)
+#pragma unroll
+              for (int u = 0; u < STEP * (int)sizeof(T) / 32; ++u)
+                store_sector((uint8_t*)(rows + lane * kp.ldy + n0 + c) + 32 * u,
+                             reinterpret_cast<const uint32_t*>(o) + 8 * u);
+            continue;
+          }
           // 16-byte unit u of row r sits at unit u ^ (r / 2 & 3): neither the
           // row owner's writes nor the row-wise reads below meet in a bank
 #pragma unroll
@@ -342,6 +362,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) arrive_remote(map_to_rank(smem_u32(&acc_empty[buf]), 0));
         }
+        if (direct) continue;
         __syncwarp();
         if (kp.vec && n0 + c0 + CW <= kp.out) {
 #pragma unroll
@@ -421,6 +442,7 @@ cudaError_t pair_int8(const gptq_int8_tokens_t* x, int64_t tokens, int64_t in, c
   kp.out = (int)out;
   kp.act = act;
   kp.vec = (uintptr_t)Y % 16 == 0 && (ldy * (yt == GPTQ_F32 ? 4 : 2)) % 16 == 0;
+  kp.vec32 = (uintptr_t)Y % 32 == 0 && (ldy * (yt == GPTQ_F32 ? 4 : 2)) % 32 == 0;
   kp.status = status;
   kp.ktiles = (int)((in + kBK - 1) / kBK);
   kp.bn = bn;

@@ -189,6 +189,35 @@ def test_strided_operands(lib):
         _within(lib.linear_int8(wide[rows, 5:165], dl), p, R.linear_tol(p, None, BF16))
 
 
+@pytest.mark.parametrize("tokens,in_,out", [(2, 64, 100), (40, 96, 300), (300, 256, 520), (700, 384, 1000), (1000, 128, 513)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("pad,first", [(16, 0), (24, 8), (7, 3), (32, 16)])
+def test_results_into_wider_buffers(lib, tokens, in_, out, dtype, pad, first):
+    """Y's rows on 32-byte, 16-byte and no boundaries; what lies around them is
+    left alone."""
+    rng = _rng(tokens, out, pad)
+    layer = R.random_layer(rng, out, in_)
+    dl = lib.Int8Layer(*(torch.from_numpy(a).cuda() for a in layer[:2]))
+    x = _values(rng, tokens, in_, BF16)
+    q, s = R.quantize(x.float().numpy())
+    t = lib.quantize_tokens(x.cuda())
+    ld = (out + 15) // 16 * 16 + pad + first
+    for gated in (False, True):
+        buf = torch.full((tokens + 2, ld), 7.0, dtype=dtype, device="cuda")
+        Y = buf[1:-1, first:first + out]
+        if gated:
+            lib.gptq_matmul_int8_gated(t, dl, dl, Y)
+            want = lib.gated_int8(t, dl, dl, dtype=dtype)
+        else:
+            lib.gptq_matmul_int8(t, dl, Y)
+            want = lib.linear_int8(t, dl, dtype=dtype)
+            p = R.product(q, s, layer)
+            _within(Y, p, R.linear_tol(p, None, dtype))
+        assert torch.equal(Y, want)
+        Y.fill_(7.0)
+        assert bool((buf == 7.0).all())
+
+
 def test_offsets_beyond_32_bits(lib):
     """70000 tokens of 32768: the codes' last rows lie past 2^31 bytes, the
     result's past 2^32."""
