@@ -33,10 +33,6 @@ __device__ __forceinline__ void raise_status(uint32_t* st, uint32_t flag) {
 // ordering stays transitive along the stream.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// The other side: lets a kernel launched this way behind this one begin (its
-// wait above still lasts until this kernel has completed).
-__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // Upper bound on any device-side spin (nanoseconds of %globaltimer).  A
 // legitimate wait in these kernels lasts well under 100 ms; a wait that
 // reaches the bound is a bug, and the kernel records ST_TIMEOUT and unwinds.

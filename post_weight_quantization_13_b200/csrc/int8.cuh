@@ -284,6 +284,9 @@ __device__ __forceinline__ void let_copies_land() {
   }
 }
 
+// Lets the kernel behind this one (launched to overlap it) begin its set-up.
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ------------------------------------------------------------ token quantizer
 // The largest magnitude of a row is taken on the bit patterns, where NaN and
 // infinity sort above every finite value.  16-bit types: both halves of a
