@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kMaxStages = 8;            // of a streaming kernel's ring
 constexpr int kStreamChunks = 2;         // chunks of eight elements a thread of the streaming norm has
-constexpr int kStreamMin = 1024;         // elements of the narrowest rows the streaming kernels take
+constexpr int kStreamMin = 8192;         // elements of rows from which the streaming kernels take them
 constexpr int kSmemPerSm = 227 * 1024;
 
 // A thread's chunks of a row: eight neighbouring elements each.  Rows on 16-byte
@@ -321,9 +321,8 @@ struct Vector {
 
 // A norm's bias in the streaming kernel, where the registers are full: in shared
 // memory, each thread's chunks written and read by itself; where there is no
-// room (at null), fetched when it is used.  (Two layer norms a row: 4096 x 8192
-// 112 us with both biases from L2 for every row, 92 from here; 8192 x 4096 84
-// and 78.)
+// room (at null), fetched when it is used.  (Two layer norms a row, 2000 x 14000:
+// 91 us with both biases from L2 for every row, 80 from here.)
 template <typename T, int NV, bool kShift>
 struct SharedVector {
   Vector<T, NV, false, kShift> from;
@@ -469,8 +468,11 @@ __device__ __forceinline__ void norm_token(const Cut<kShift>& cut, const NormPar
   }
 }
 
-// A row a warp or a block, every operand straight to registers: few tokens or
-// narrow rows (one token of 4096 takes 2.3 us, all latency).
+// A row a warp or a block, every operand straight to registers: few tokens, or
+// rows of which several blocks fit an SM, so that one's loads and reductions
+// overlap the others'.  One token of 4096 takes 2.3 us, all latency; 8192 of
+// them with both norms and a gate 55, bound by memory that reads and writes in
+// turn (the bytes alone 42).
 template <typename T, typename H, int NV, bool kShift>
 __global__ void __launch_bounds__(1024) norm_tokens_kernel(const __grid_constant__ NormParams p) {
   __shared__ uint32_t buf[64];
@@ -504,11 +506,9 @@ __global__ void __launch_bounds__(1024) norm_tokens_kernel(const __grid_constant
 // ------------------------------------------------------- streaming kernels
 // Many tokens of wide rows: persistent blocks whose rows arrive in a ring of
 // shared-memory stages by bulk copies, the next rows' while this one is worked
-// on, so memory never waits for a statistic.  Bound by memory where rows are
-// read and written in turn (8192 x 4096 bf16, both norms and a gate: 54 to 57 us
-// for 268 MB; more warps do not help), by its four reductions a row where rows
-// are so wide that one block fills an SM (1001 x 11008 layer norms: 43 us, the
-// bytes alone 24).
+// on, so memory does not wait for a statistic.  What bounds the norm is its four
+// reductions a row, since one block fills an SM (1001 x 11008 layer norms: 43
+// us, the bytes alone 24).
 struct Ring {
   uint8_t* at;
   uint64_t* full;
@@ -648,8 +648,7 @@ __global__ void __launch_bounds__(1024) quantize_stream_kernel(const T* __restri
 // elements (reductions, addresses) bound the kernel; unrolled over 32 the code
 // left the instruction cache; and in loops over shared memory the weights had
 // to come from L2 for every row, where here they stay in registers for all of
-// a block's rows (8192 rows of 4096 bf16 with both norms and a gate: 87, 68
-// and 76 us).
+// a block's rows.
 template <typename T, typename H, bool kShift, int MaxThreads>
 __global__ void __launch_bounds__(MaxThreads, 1) norm_stream_kernel(const __grid_constant__ NormParams p) {
   constexpr int NV = kStreamChunks;
@@ -675,7 +674,7 @@ __global__ void __launch_bounds__(MaxThreads, 1) norm_stream_kernel(const __grid
     for (int s = 0; s < stages && blockIdx.x + (int64_t)s * gridDim.x < p.tokens; ++s)
       fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
   RowReduce red(buf);
-  // the grid is a multiple of eight: all of a block's rows are aligned alike
+  // a shifted grid is a multiple of eight: all of a block's rows are aligned alike
   const int64_t t0 = blockIdx.x;
   const int slots = 8 * NV * (int)blockDim.x;
   const Cut<kShift> cut = p.y ? Cut<kShift>((const T*)p.y + t0 * p.ldy, d, slots)
@@ -766,9 +765,18 @@ int row_chunks(int d, int64_t tokens, int sms) {
   return tokens > 4 * sms ? (d <= 256 ? 1 : 2) : (d <= 1024 * 8 ? 1 : 2);
 }
 
-// Whether a streaming kernel takes the call: rows a block wide, and enough of
-// them to fill every block's ring more than once.
-bool streams(int d, int64_t tokens, int sms) { return d >= kStreamMin && tokens > 4 * sms; }
+// Whether a streaming kernel takes the call: enough rows to fill every block's
+// ring more than once, and of those the rows so wide that few of their blocks
+// fit an SM.  Narrower rows overlap better as many blocks of one row each (norms
+// of 8000 x 4096 bf16 and quantized: streaming 60.9 us, else 51.6; 2000 x 8192
+// 41.3 and 32.6; but with both norms and a gate 2000 x 11008 45 and 61).  The
+// quantizer does so little for a row that of 16-bit types it streams from some
+// size on (8000 x 4096: 23.6 us, else 27.7; 2000 x 4096: 7.6 and 7.4; fp32
+// 8000 x 4096 29.8 and 28.3).
+bool streams_norm(int d, int64_t tokens, int sms) { return d > kStreamMin && tokens > 4 * sms; }
+bool streams_quantizer(int d, size_t size, int64_t tokens, int sms) {
+  return tokens > 4 * sms && (d >= kStreamMin || (size == 2 && d >= 1024 && tokens * d > 12000000));
+}
 
 // Bytes of a row in a stage (Source::room).
 int row_room(int d, size_t size, bool shift) {
@@ -806,7 +814,7 @@ cudaError_t launch_quantize(const T* X, int64_t tokens, int d, int64_t ldx, int8
                             int32_t* sum, cudaStream_t st) {
   const bool vec = (uintptr_t)X % 16 == 0 && (ldx * (int64_t)sizeof(T)) % 16 == 0;
   const int sms = device_info().sms;
-  if (streams(d, tokens, sms)) {
+  if (streams_quantizer(d, sizeof(T), tokens, sms)) {
     const bool whole = vec && d % 8 == 0;
     const int stage_bytes = (int)round_up(row_room(d, sizeof(T), !whole), 128);
     const StreamShape shape(span(d, !whole), 32, 32, stage_bytes);
@@ -867,7 +875,7 @@ template <typename T, typename H>
 cudaError_t launch_norm(NormParams& p, cudaStream_t st) {
   const int sms = device_info().sms;
   const bool whole = p.aligned && p.d % 8 == 0;
-  if (p.weight && span(p.d, !whole) <= 1024 * 8 * kStreamChunks && streams(p.d, p.tokens, sms)) {
+  if (p.weight && span(p.d, !whole) <= 1024 * 8 * kStreamChunks && streams_norm(p.d, p.tokens, sms)) {
     p.stage_bytes = (int)round_up(row_room(p.d, sizeof(H), !whole) +
                                       ((p.y ? 1 : 0) + (p.gate && p.ldgate ? 1 : 0)) * row_room(p.d, sizeof(T), !whole),
                                   128);

@@ -44,6 +44,7 @@ def _untouched(buf, rows, cols, fill=7.0):
     (33, 4096, F16, 8), (4, 11008, F16, 0), (2, 16384, BF16, 0), (3, 16385, F32, 0), (2, 32768, F32, 0),
     (1001, 77, BF16, 0), (6, 32767, F16, 0),
     # many rows: the streaming kernel, its ring going round, and what it leaves to the other
+    (3100, 4096, BF16, 0), (3100, 4001, F16, 0), (12000, 1025, BF16, 3), (601, 8192, F32, 0), (700, 9001, F32, 0),
     (3001, 1024, BF16, 8), (1500, 4096, F32, 4), (2000, 11008, F16, 0), (700, 32768, F32, 0), (900, 1032, F16, 1),
     (40000, 512, BF16, 0), (1300, 1025, F16, 0), (700, 4001, BF16, 0), (601, 11007, F32, 0), (800, 2000, BF16, 3),
     (3, 32768, F16, 3), (3, 16383, BF16, 0), (2500, 509, F16, 0), (2500, 254, BF16, 1), (900, 32765, F16, 0),
@@ -247,6 +248,9 @@ NORMS = [  # tokens, d, type, residual type, kind, post, gate, alpha, beta, pad
     (1203, 11008, F16, F32, "layer", True, "token", 0.7, 1.0, 0), (700, 16384, BF16, BF16, "rms", False, None, 1, 1, 0),
     (601, 32768, BF16, F32, "rms", True, "channel", 1, 1, 0), (999, 4096, F32, F32, "rms", True, "token", 1, 1, 0),
     (2000, 4100, BF16, BF16, "rms", True, "channel", 1, 1, 0), (700, 4001, BF16, BF16, "layer", True, "token", 1, 1, 0),
+    (650, 9001, BF16, BF16, "layer", True, "token", 1, 1, 0), (700, 12289, F16, F32, "layer", True, None, 1, 1, 0),
+    (601, 8200, F32, F32, "rms", True, "token", 1, 1, 0), (640, 9003, F16, F16, "rms", True, "channel", 1, 1, 5),
+    (600, 14000, F16, F16, "layer", True, "token", 1, 1, 0), (610, 8193, F32, F32, "layer", True, "channel", 1, 1, 0),
     (601, 11007, F16, F32, "rms", True, "channel", 0.7, 1, 0), (650, 1031, F32, F32, "layer", False, "token", 1, 1, 1),
     (600, 16383, BF16, F32, "rms", False, None, 1, 1, 0), (3, 32768, BF16, F32, "rms", True, "token", 1, 1, 3),
     (3, 16380, F16, F16, "layer", True, None, 1, 1, 1), (4, 8190, F16, F16, "rms", True, "channel", 1, 1, 1),
@@ -300,7 +304,8 @@ def test_norm_first_block_and_in_place(lib):
     assert got is c and torch.equal(got, want) and torch.equal(gx, wx)
 
 
-@pytest.mark.parametrize("tokens,d,offset", [(7, 333, 1), (5, 40, 3), (700, 1024, 1), (601, 4001, 5), (650, 2051, 7)])
+@pytest.mark.parametrize("tokens,d,offset", [(7, 333, 1), (5, 40, 3), (700, 1024, 1), (601, 4001, 5), (650, 2051, 7),
+                                             (601, 9001, 5), (620, 8203, 7), (3000, 4099, 1)])
 @pytest.mark.parametrize("dtype", [F16, F32])
 def test_rows_that_start_anywhere(lib, tokens, d, offset, dtype):
     """Tensors that begin and end inside a 16-byte unit, their surroundings
