@@ -27,7 +27,7 @@
 //
 // Measured: 16384 tokens of 4096 > 11008 492 us in a burst (3.0e15 operations
 // a second, 0.89 of twice the measured bf16 rate), 600 us sustained, where the
-// power limit holds the clock down; gated 4096 tokens of 4096 > 11008 240 us.
+// power limit holds the clock down; gated 4096 tokens of 4096 > 11008 233 us.
 #include <algorithm>
 #include <cstring>
 

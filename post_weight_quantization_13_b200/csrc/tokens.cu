@@ -471,7 +471,7 @@ __device__ __forceinline__ void norm_token(const Cut<kShift>& cut, const NormPar
 // A row a warp or a block, every operand straight to registers: few tokens, or
 // rows of which several blocks fit an SM, so that one's loads and reductions
 // overlap the others'.  One token of 4096 takes 2.3 us, all latency; 8192 of
-// them with both norms and a gate 55, bound by memory that reads and writes in
+// them with both norms and a gate 57, bound by memory that reads and writes in
 // turn (the bytes alone 42).
 template <typename T, typename H, int NV, bool kShift>
 __global__ void __launch_bounds__(1024) norm_tokens_kernel(const __grid_constant__ NormParams p) {
