@@ -10,28 +10,22 @@
 // took 13.9 us, now 10.8; of the gated 4096 x 11008 20.4, now 18.0, where the
 // bytes alone take 14.)  A block owns a contiguous range of channels, which
 // divide evenly over the SMs whatever their number.  Two groups of 256 threads
-// take batches of eight rows in turn, one at its sums while the other
-// multiplies.  A group's threads split k: each multiplies (dp4a) its own
-// columns of the rows with its own columns of the tokens.  A row's sum then
-// costs its share of one transposed warp reduction for the batch (N values in
-// N - 1 + log2(32 / N) exchanges) and of one exchange between the warps.
-#include <algorithm>
-
+// take batches of eight rows in turn, each from a ring of its own (rows_ring.cuh
+// says why), one at its sums while the other multiplies.  A group's threads
+// split k: each multiplies (dp4a) its own columns of the rows with its own
+// columns of the tokens.  A row's sum then costs its share of one transposed
+// warp reduction for the batch (N values in N - 1 + log2(32 / N) exchanges) and
+// of one exchange between the warps.
 #include "gemm.cuh"
 #include "int8.cuh"
 #include "internal.cuh"
+#include "rows_ring.cuh"
 
 namespace gptq {
 namespace {
 
-constexpr int kThreads = 256;          // of a group, whose threads split k
+using namespace rows;
 constexpr int kWarps = kThreads / 32;
-constexpr int kGroups = 2;             // that take the batches in turn
-constexpr int kBatch = 8;              // weight rows of a reduction
-constexpr int kSlice = kThreads * 16;  // columns of one step
-constexpr int kMaxSteps = 3;           // in <= 12288: two batches of the widest rows nearly fill the ring
-constexpr int kMaxSlots = 40;          // of the ring
-constexpr int kSmem = 227 * 1024 - 6 * 1024;  // dynamic shared memory; the rest is the static arrays'
 
 struct RowsParams {
   const void* x;
@@ -48,8 +42,7 @@ struct RowsParams {
   int yt;
   int64_t ldy;
   int tokens, out, in, act;
-  int rows;  // the most channels a block owns
-  int slots, slot_bytes, group, row_bytes, dense;
+  Plan plan;
   uint32_t* status;
   int vec;  // x's rows start on 16-byte boundaries
 };
@@ -163,27 +156,31 @@ __global__ void __launch_bounds__(kGroups * kThreads + 32, 1) int8_rows_kernel(c
   __shared__ int tsum[T];
   __shared__ uint32_t exchange[kWarps][T];
   __shared__ int sums[kGroups][2][kWarps][N];
-  __shared__ uint64_t full[kMaxSlots], empty[kMaxSlots];
+  __shared__ uint64_t full[kGroups * kMaxSlots], empty[kGroups * kMaxSlots];
+  static_assert(sizeof(tscale) + sizeof(tsum) + sizeof(exchange) + sizeof(sums) + sizeof(full) + sizeof(empty) <= kStatic,
+                "static arrays");
 
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
-  const int steps = (kp.in + kSlice - 1) / kSlice, slots = kp.slots, slot_bytes = kp.slot_bytes;
-  uint8_t* const ring = smem;                                          // [slots][slot_bytes]
-  int4* const codes = (int4*)(smem + (size_t)slots * slot_bytes);      // [T][steps][thread]
-  // the block's channels' scales, zeros and bias: fetched once up front, since
-  // a load in a batch's epilogue would hold up the whole block for its latency
-  float* const wscale = (float*)(codes + (size_t)T * steps * kThreads);  // [G][rows]
-  int* const wzero = (int*)(wscale + G * kp.rows);                       // [G][rows]
-  float* const bias = (float*)(wzero + G * kp.rows);                     // [rows]
+  const int steps = (kp.in + kSlice - 1) / kSlice;
+  const int slots = kp.plan.slots, slot_bytes = kp.plan.slot_bytes, own = kp.plan.rows;
+  uint8_t* const ring = smem;                                                // [group][slots][slot_bytes]
+  int4* const codes = (int4*)(smem + (size_t)kGroups * slots * slot_bytes);  // [T][steps][thread]
+  // the block's channels' scales, zeros and (plain) bias: fetched once up front,
+  // since a load in a batch's epilogue would hold up the whole block for its
+  // latency
+  float* const wscale = (float*)(codes + (size_t)T * steps * kThreads);  // [G][own]
+  int* const wzero = (int*)(wscale + G * own);                           // [G][own]
+  float* const bias = (float*)(wzero + G * own);                         // [own]
   const int n_begin = (int)((int64_t)kp.out * blockIdx.x / gridDim.x);
   const int n_end = (int)((int64_t)kp.out * (blockIdx.x + 1) / gridDim.x);
   const int batches = (n_end - n_begin + R - 1) / R;
 
   // A slot: `group` rows of each of the batch's projections, one after another
   // at row_bytes.
-  const int group = kp.group, row_bytes = kp.row_bytes;
+  const int group = kp.plan.group, row_bytes = kp.plan.row_bytes, dense = kp.plan.dense;
   if (warp == kGroups * kWarps) {
     // ------------------------------------------------------------ producer
-    for (int s = lane; s < slots; s += 32) {
+    for (int s = lane; s < kGroups * slots; s += 32) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], kWarps);
     }
@@ -192,10 +189,18 @@ __global__ void __launch_bounds__(kGroups * kThreads + 32, 1) int8_rows_kernel(c
     named_bar_sync(2, kThreads + 32);
     const uint32_t leader = elect_lane();
     const uint32_t ring0 = smem_u32(ring), full0 = smem_u32(full), empty0 = smem_u32(empty);
-    int slot = 0;
-    uint32_t phase = 1;
+    Cursor at, other;  // in this batch's ring and in the other one
+    at.phase = other.phase = 1;
+    int base = 0;
     for (int c = 0; c < n_end - n_begin; c += group) {
-      if (!wait_at(empty0 + 8 * slot, phase)) {
+      if (c > 0 && c % R == 0) {
+        const Cursor next = other;
+        other = at;
+        at = next;
+        base = slots - base;
+      }
+      const int slot = base + at.slot;
+      if (!wait_at(empty0 + 8 * slot, at.phase)) {
         raise_status(kp.status, ST_TIMEOUT);
         let_copies_land();
         break;
@@ -205,23 +210,20 @@ __global__ void __launch_bounds__(kGroups * kThreads + 32, 1) int8_rows_kernel(c
       const bool last = n + rows == kp.out;
       const uint32_t row16 = (uint32_t)(kp.in + 15) & ~15u, tail = last ? (uint32_t)kp.in & ~15u : row16;
       expect_at(leader, full0 + 8 * slot,
-                kp.dense ? G * ((rows - 1) * (uint32_t)row_bytes + tail) : G * ((rows - 1) * row16 + tail));
+                dense ? G * ((rows - 1) * (uint32_t)row_bytes + tail) : G * ((rows - 1) * row16 + tail));
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const uint32_t at = ring0 + slot * kp.slot_bytes + g * group * row_bytes;
+        const uint32_t to = ring0 + slot * slot_bytes + g * group * row_bytes;
         const int8_t* from = kp.w[g] + n * kp.ldw[g];
-        if (kp.dense) {  // rows follow one another as the slot wants them
-          bulk_load_at(leader, at, from, (rows - 1) * (uint32_t)row_bytes + tail, full0 + 8 * slot);
+        if (dense) {  // rows follow one another as the slot wants them
+          bulk_load_at(leader, to, from, (rows - 1) * (uint32_t)row_bytes + tail, full0 + 8 * slot);
         } else {
           for (int r = 0; r < rows; ++r)
-            bulk_load_at(leader, at + r * row_bytes, from + r * kp.ldw[g], r + 1 < rows ? row16 : tail,
+            bulk_load_at(leader, to + r * row_bytes, from + r * kp.ldw[g], r + 1 < rows ? row16 : tail,
                          full0 + 8 * slot);
         }
       }
-      if (++slot == slots) {
-        slot = 0;
-        phase ^= 1;
-      }
+      at.advance(1, slots);
     }
     __syncwarp();
   } else {
@@ -231,10 +233,10 @@ __global__ void __launch_bounds__(kGroups * kThreads + 32, 1) int8_rows_kernel(c
       for (int i = threadIdx.x; i < n_end - n_begin; i += kGroups * kThreads) {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          wscale[g * kp.rows + i] = __ldg(kp.wscale[g] + n_begin + i);
-          wzero[g * kp.rows + i] = kp.wzero[g] ? __ldg(kp.wzero[g] + n_begin + i) : 0;
+          wscale[g * own + i] = __ldg(kp.wscale[g] + n_begin + i);
+          wzero[g * own + i] = kp.wzero[g] ? __ldg(kp.wzero[g] + n_begin + i) : 0;
         }
-        bias[i] = G == 1 && kp.bias ? __ldg(kp.bias + n_begin + i) : 0.f;
+        if (G == 1) bias[i] = kp.bias ? __ldg(kp.bias + n_begin + i) : 0.f;
       }
     };
     if (who > 0) {
@@ -269,18 +271,10 @@ __global__ void __launch_bounds__(kGroups * kThreads + 32, 1) int8_rows_kernel(c
     vectors();
     named_bar_sync(3, kGroups * kThreads);
 
-    const uint32_t full0 = smem_u32(full);
-    const int per_batch = R / group;  // slots
-    int slot = 0;
-    uint32_t phase = 0;
-    auto advance = [&](int by) {
-      slot += by;
-      while (slot >= slots) {
-        slot -= slots;
-        phase ^= 1;
-      }
-    };
-    advance(who * per_batch);
+    uint8_t* const mine = ring + (size_t)who * slots * slot_bytes;  // the group's ring
+    uint64_t* const my_empty = empty + who * slots;
+    const uint32_t my_full = smem_u32(full + who * slots);
+    Cursor at;
     bool gave_up = false;  // after a wait that gave up the block runs on without waiting, on whatever is there
     int half = 0;
     for (int batch = who; batch < batches; batch += kGroups, half ^= 1) {
@@ -293,10 +287,10 @@ __global__ void __launch_bounds__(kGroups * kThreads + 32, 1) int8_rows_kernel(c
       const int4* row[kBatch];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int at = r & (group - 1);  // a batch is whole slots
-        if (at == 0 && r < rows) {
-          if (r > 0) advance(1);
-          if (!gave_up && !wait_at(full0 + 8 * slot, phase)) {
+        const int in_slot = r & (group - 1);  // a batch is whole slots
+        if (in_slot == 0 && r < rows) {
+          if (r > 0) at.advance(1, slots);
+          if (!gave_up && !wait_at(my_full + 8 * at.slot, at.phase)) {
             gave_up = true;
             raise_status(kp.status, ST_TIMEOUT);
           }
@@ -304,7 +298,7 @@ __global__ void __launch_bounds__(kGroups * kThreads + 32, 1) int8_rows_kernel(c
 #pragma unroll
         for (int g = 0; g < G; ++g)
           row[g * R + r] =
-              r < rows ? (const int4*)(ring + (size_t)slot * kp.slot_bytes + (g * group + at) * row_bytes) + tid
+              r < rows ? (const int4*)(mine + (size_t)at.slot * slot_bytes + (g * group + in_slot) * row_bytes) + tid
                        : row[g * R + r - 1];
       }
       for (int step = 0; step < steps; ++step) {
@@ -332,10 +326,10 @@ __global__ void __launch_bounds__(kGroups * kThreads + 32, 1) int8_rows_kernel(c
       // back from the batch's last slot to its first
       const int held = (rows + group - 1) / group;
       for (int j = 0; j < held; ++j) {
-        const int s = slot - j + (slot < j ? slots : 0);
-        if (lane == 0) mbar_arrive(&empty[s]);
+        const int s = at.slot - j + (at.slot < j ? slots : 0);
+        if (lane == 0) mbar_arrive(&my_empty[s]);
       }
-      advance(per_batch - (held - 1) + (kGroups - 1) * per_batch);
+      at.advance(1, slots);
       const int sum = warp_sums<N>(acc);
       if (lane % (32 / N) == 0) sums[who][half][warp % kWarps][lane / (32 / N)] = sum;
       // The other half of sums is written before the group's next barrier, this
@@ -350,20 +344,20 @@ __global__ void __launch_bounds__(kGroups * kThreads + 32, 1) int8_rows_kernel(c
             int total = 0;
 #pragma unroll
             for (int v = 0; v < kWarps; ++v) total += sums[who][half][v][g * R * T + tid];
-            y[g] = scaled(total, wzero[g * kp.rows + c], tsum[t], tscale[t], wscale[g * kp.rows + c]);
+            y[g] = scaled(total, wzero[g * own + c], tsum[t], tscale[t], wscale[g * own + c]);
           }
           float o = y[0];
           if (G == 2)
             o = activate(y[0], kp.act) * y[G - 1];
           else
             o += bias[c];
-          const int64_t at = t * kp.ldy + n;
+          const int64_t to = t * kp.ldy + n;
           if (kp.yt == GPTQ_F16)
-            ((__half*)kp.Y)[at] = from_f32<__half>(o);
+            ((__half*)kp.Y)[to] = from_f32<__half>(o);
           else if (kp.yt == GPTQ_BF16)
-            ((__nv_bfloat16*)kp.Y)[at] = from_f32<__nv_bfloat16>(o);
+            ((__nv_bfloat16*)kp.Y)[to] = from_f32<__nv_bfloat16>(o);
           else
-            ((float*)kp.Y)[at] = o;
+            ((float*)kp.Y)[to] = o;
         }
       }
     }
@@ -373,27 +367,12 @@ __global__ void __launch_bounds__(kGroups * kThreads + 32, 1) int8_rows_kernel(c
 
 template <int G, int T>
 cudaError_t launch(RowsParams& kp, cudaStream_t st, int sms) {
-  const int grid = std::min(sms, kp.out);
-  kp.rows = (kp.out + grid - 1) / grid;
-  const int steps = (kp.in + kSlice - 1) / kSlice;
-  const int fixed = T * steps * kThreads * 16 + (2 * G + 1) * kp.rows * 4;
-  // Slots of up to 32 KB (a copy's issue takes as long as some KB of it): 1, 2,
-  // 4 or 8 channels, as a batch is whole slots.  Rows that lie closely one
-  // after another come in one copy, padding and all.
-  kp.dense = 1;
-  for (int g = 0; g < G; ++g) kp.dense &= kp.ldw[g] == kp.ldw[0] && kp.ldw[g] <= kp.in + 127;
-  kp.row_bytes = kp.dense ? (int)kp.ldw[0] : (kp.in + 15) / 16 * 16;
-  kp.group = kBatch / G;
-  while (kp.group > 1 && G * kp.group * kp.row_bytes > 32768) kp.group /= 2;
-  kp.slot_bytes = (G * kp.group * kp.row_bytes + 127) / 128 * 128;
-  // at least the one batch that a group holds, and two (one a group) but for
-  // the widest rows with padding
-  kp.slots = std::min(kMaxSlots, (kSmem - fixed) / kp.slot_bytes);
-  const int smem = fixed + kp.slots * kp.slot_bytes;
+  const bool same = G == 1 || kp.ldw[0] == kp.ldw[1];
+  kp.plan = plan(G, T, kp.in, kp.out, same ? kp.ldw[0] : 0, sms);
   const void* f = (const void*)int8_rows_kernel<G, T>;
   cudaError_t e = ensure_smem_limit(f, kSmem);
   if (e != cudaSuccess) return e;
-  int8_rows_kernel<G, T><<<grid, kGroups * kThreads + 32, smem, st>>>(kp);
+  int8_rows_kernel<G, T><<<kp.plan.grid, kGroups * kThreads + 32, kp.plan.smem, st>>>(kp);
   note_launch();
   return cudaGetLastError();
 }

@@ -1,0 +1,62 @@
+"""The 8-bit serving calls where sizes, values and callers meet their limits."""
+import numpy as np
+import pytest
+import torch
+
+import serving_ref as R
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+
+
+def _within(got, want, tol):
+    off = (got.double() - want).abs()
+    bad = ~(off <= tol)
+    assert not bool(bad.any()), (int(bad.sum()), bad.nonzero()[:3].tolist(), float((off / tol).max()))
+
+
+# ------------------------------------------------------------ one or two tokens
+def _wide_layer(gen, out, in_, pad):
+    """Full-range codes in rows of in_ + pad bytes, on the device."""
+    w = torch.randint(-128, 128, (out, (in_ + 15) // 16 * 16 + pad), generator=gen, device="cuda", dtype=torch.int8)
+    scale = torch.rand(out, generator=gen, device="cuda") * 1e-4 + 1e-5
+    zero = torch.randint(-128, 128, (out,), generator=gen, device="cuda", dtype=torch.int32)
+    return w[:, :in_], scale, zero
+
+
+def _sums(q, layer, rows=4096):
+    """The scaled product in float64 (sums of integers below 2^53: exact)."""
+    w, scale, zero = layer
+    total = torch.cat([q @ w[i:i + rows].double().T for i in range(0, w.shape[0], rows)], 1)
+    return (total - q.sum(1, keepdim=True) * zero.double()) * scale.double()
+
+
+@pytest.mark.parametrize("tokens,in_,out,pad", [
+    # the widest rows with the most channels, unpadded and padded: rings that hold just a batch each
+    (2, 12288, 40000, 0), (2, 12288, 65535, 0), (2, 12288, 65535, 112), (1, 12288, 65535, 96), (2, 12280, 65535, 0),
+    # rings of odd numbers of slots
+    (2, 11008, 4096, 0), (1, 11008, 4096, 0), (2, 8208, 5000, 0), (1, 9000, 3001, 16), (2, 4112, 20000, 0),
+])
+@pytest.mark.parametrize("gated", [False, True])
+def test_wide_rows_and_many_channels_of_one_and_two_tokens(lib, tokens, in_, out, pad, gated):
+    gen = torch.Generator("cuda").manual_seed(in_ + out + pad)
+    x = torch.randn(tokens, in_, generator=gen, device="cuda").to(BF16)
+    a, b = _wide_layer(gen, out, in_, pad), _wide_layer(gen, out, in_, pad)
+    t = lib.quantize_tokens(x)
+    q = t.q.double()
+    g, u = (_sums(q, l) * t.scale.double()[:, None] for l in (a, b))
+    for _ in range(5):
+        if not gated:
+            y = lib.linear_int8(t, a, dtype=F32)
+            _within(y, g, (5 * R.U32 * g.abs()) * 1.01 + R.FLOOR[F32])
+        else:
+            y = lib.gated_int8(t, a, b, dtype=F32)
+            # silu's relative error: see serving_ref.act_tol
+            z = g.abs()
+            act = g / (1 + torch.exp(-g))
+            off = act.abs() * ((1 + z) * 4 * R.U32 + z * 6 * R.U32 + (6 + 1.173 * z) * 2.0 ** -23) + 2e-36
+            _within(y, act * u, (off * u.abs() + 6 * R.U32 * (act * u).abs()) * 1.01 + R.FLOOR[F32])
+        # and quantized on the way: the same bits
+        assert torch.equal(y, lib.gated_int8(x, a, b, dtype=F32) if gated else lib.linear_int8(x, a, dtype=F32))
+    lib.gptq_int8_status()
