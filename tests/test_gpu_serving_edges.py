@@ -60,3 +60,28 @@ def test_wide_rows_and_many_channels_of_one_and_two_tokens(lib, tokens, in_, out
         # and quantized on the way: the same bits
         assert torch.equal(y, lib.gated_int8(x, a, b, dtype=F32) if gated else lib.linear_int8(x, a, dtype=F32))
     lib.gptq_int8_status()
+
+
+# ------------------------------------------------------------------ gelu's tail
+@pytest.mark.parametrize("tokens", [1, 2, 20, 300])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gelu_keeps_its_relative_accuracy_where_it_vanishes(lib, tokens, dtype):
+    """Gate values from -12 (gelu -2e-32) to 3, one product of each."""
+    in_, out = 32, 600
+    q = torch.zeros(tokens, in_, dtype=torch.int8, device="cuda")
+    q[:, 0] = 1
+    scale = (1 + torch.arange(tokens, device="cuda") / (4.0 * tokens)).float()
+    x = lib.Int8Tokens(q, scale, torch.ones(tokens, dtype=torch.int32, device="cuda"))
+    w = torch.zeros(out, in_, dtype=torch.int8, device="cuda")
+    w[:, 0] = torch.arange(out, device="cuda") % 160 - 127
+    gate = (w, torch.full((out,), 9.6 / 127, device="cuda"))
+    one = torch.zeros_like(w)
+    one[:, 0] = 1
+    up = (one, torch.full((out,), 0.75, device="cuda"))
+    y = lib.gated_int8(x, gate, up, act="gelu", dtype=dtype)
+    g = scale.double()[:, None] * (w[:, 0].double() * gate[1].double())
+    want = 0.5 * g * torch.special.erfc(-g / 2 ** 0.5) * (0.75 * scale.double()[:, None])
+    # g is 2 roundings off and erfc's argument 2 more; the condition number of gelu is at most g^2 + 3 below zero
+    # (Mills' ratio) and 2 above.  erfcf is within 4 units of 2^-23 (documented); 6 roundings around it.
+    tol = want.abs() * ((g ** 2 + 3) * 4 * R.U32 + 4 * 2.0 ** -23 + 6 * R.U32 + R.U[dtype]) * 1.01 + R.FLOOR[dtype]
+    _within(y, want, tol)
