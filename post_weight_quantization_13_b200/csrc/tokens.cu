@@ -9,7 +9,8 @@
 // and the two or three statistics of a row (sums of squares, means, the
 // largest magnitude) are reduced by warp shuffles and one shared-memory
 // exchange each.  All statistics are fp32; a mean is subtracted before the
-// squares are summed, so a layer norm loses nothing to cancellation.
+// squares are summed, and what its rounding left is taken off after
+// (norm_statistic), so that rows far from zero keep their accuracy.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -26,6 +27,7 @@ constexpr int kMaxStages = 8;            // of a streaming kernel's ring
 constexpr int kStreamChunks = 2;         // chunks of eight elements a thread of the streaming norm has
 constexpr int kStreamMin = 8192;         // elements of rows from which the streaming kernels take them
 constexpr int kSmemPerSm = 227 * 1024;
+constexpr int kExchange = 2 * 64;        // words of a row's reductions
 
 // A thread's chunks of a row: eight neighbouring elements each.  Rows on 16-byte
 // boundaries are cut at multiples of eight.  Else (kShift: odd sizes, where
@@ -165,13 +167,13 @@ __device__ __forceinline__ Raw8<T> read_across(const T* row, int e, int d) {
 // barrier each is enough: a buffer is written again only after the barrier of
 // the reduction in between.
 struct RowReduce {
-  uint32_t* buf;  // [2][32]
+  uint32_t* buf;  // [kExchange]: two buffers, each of two words for a warp
   int parity;
   __device__ __forceinline__ RowReduce(uint32_t* b) : buf(b), parity(0) {}
   template <typename V, typename F>
   __device__ __forceinline__ V exchange(V warp_value, V identity, F combine) {
     if (blockDim.x <= 32) return warp_value;
-    V* b = reinterpret_cast<V*>(buf + 32 * parity);
+    V* b = reinterpret_cast<V*>(buf + kExchange / 2 * parity);
     parity ^= 1;
     const int lane = threadIdx.x & 31;
     if (lane == 0) b[threadIdx.x >> 5] = warp_value;
@@ -194,6 +196,18 @@ struct RowReduce {
       for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
       return x;
     });
+  }
+  // Two sums through one exchange.
+  __device__ __forceinline__ float2 sum(float2 v) {
+    const auto lanes = [](float2 x) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
+        x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
+      }
+      return x;
+    };
+    return exchange(lanes(v), make_float2(0.f, 0.f), lanes);
   }
   __device__ __forceinline__ uint32_t max_u32(uint32_t v) {
     return exchange(__reduce_max_sync(0xffffffffu, v), 0u,
@@ -259,7 +273,7 @@ template <typename T, int NV, bool kShift>
 __global__ void __launch_bounds__(1024) quantize_tokens_kernel(const T* __restrict__ X, int64_t tokens, int d,
                                                                int64_t ldx, int8_t* __restrict__ q, int64_t ldq,
                                                                float* __restrict__ scale, int32_t* __restrict__ sum) {
-  __shared__ uint32_t buf[64];
+  __shared__ __align__(8) uint32_t buf[kExchange];
   __shared__ uint64_t edge[kShift ? 32 * NV : 1];
   grid_launch_dependents();  // a product behind this kernel sets up beside it
   const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -291,7 +305,6 @@ struct NormParams {
   float* scale;
   int32_t* sum;
   float alpha, beta, eps;
-  int layer;
   int stages, stage_bytes;  // of the streaming kernel
   int post_bias_at, bias_at;  // their places in its shared memory, 0: none
   uint32_t* status;
@@ -353,31 +366,52 @@ __device__ __forceinline__ void clear_past(const Cut<kShift>& cut, Pair (&v)[NV]
   }
 }
 
-// The row without its mean where that is asked for, and 1 / sqrt(mean v^2 +
-// eps).
-template <int NV, bool kShift>
+// The row without its mean for a layer norm, and 1 / sqrt(mean v^2 + eps).  A
+// mean in fp32 is off by a few roundings of its own size, which for rows far
+// from zero is much beside their spread: a row of equal values around 1000 gave
+// up to 1 for 0.  So the sum of what is left is taken with the sum of its
+// squares, in one exchange, and its mean comes off the variance and the row.
+// (Layer norms take 2 to 7 % longer for it: 8000 x 4096 before and after a
+// block 65.3 us, so 68.4.  Only where the mean is large beside the spread, by
+// a branch: 66.6, but 1001 x 11008 from the ring 47 us, so 39.7.)
+template <bool kLayer, int NV, bool kShift>
 __device__ __forceinline__ float norm_statistic(const Cut<kShift>& cut, Pair (&v)[NV][4], const NormParams& p,
                                                 RowReduce& red) {
   const float inv_d = 1.f / (float)p.d;
-  if (p.layer) {
-    Pair s(0.f);
+  Pair s(0.f), s2(0.f);
+  if (!kLayer) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) s = add2(s, v[i][u]);
-    const Pair mean(-red.sum(s.f().x + s.f().y) * inv_d);
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int u = 0; u < 4; ++u) v[i][u] = add2(v[i][u], mean);
-    clear_past<NV, kShift>(cut, v, p.d);
+      for (int u = 0; u < 4; ++u) s2 = fma2(v[i][u], v[i][u], s2);
+    return rsqrtf(fmaf(red.sum(s2.f().x + s2.f().y), inv_d, p.eps));
   }
-  Pair s2(0.f);
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) s2 = fma2(v[i][u], v[i][u], s2);
-  return rsqrtf(fmaf(red.sum(s2.f().x + s2.f().y), inv_d, p.eps));
+    for (int u = 0; u < 4; ++u) s = add2(s, v[i][u]);
+  const Pair mean(-red.sum(s.f().x + s.f().y) * inv_d);
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[i][u] = add2(v[i][u], mean);
+  clear_past<NV, kShift>(cut, v, p.d);
+  s = Pair(0.f);
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      s = add2(s, v[i][u]);
+      s2 = fma2(v[i][u], v[i][u], s2);
+    }
+  const float2 sums = red.sum(make_float2(s.f().x + s.f().y, s2.f().x + s2.f().y));
+  const float left = sums.x * inv_d, var = fmaf(-left, left, sums.y * inv_d);
+  const Pair minus(-left);  // (also outside the row, where weights, gates and biases are zero)
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[i][u] = add2(v[i][u], minus);
+  return rsqrtf((var < 0.f ? 0.f : var) + p.eps);
 }
 
 // v * r * weight (+ bias)
@@ -407,7 +441,7 @@ __device__ __forceinline__ void store_row(const Cut<kShift>& cut, T* __restrict_
 // and/or int8.  The pre-norm works on h' before it is rounded to its stored
 // type.  h(i), y(i) and gate(i) give the operands' chunks; release() is called
 // once by every thread when the whole row has been read by all of them.
-template <typename T, typename H, int NV, bool kShift, typename LoadH, typename LoadY, typename LoadGate, typename V,
+template <bool kLayer, typename T, typename H, int NV, bool kShift, typename LoadH, typename LoadY, typename LoadGate, typename V,
           typename B, typename Release>
 __device__ __forceinline__ void norm_token(const Cut<kShift>& cut, const NormParams& p, int64_t t, RowReduce& red,
                                            uint64_t (&edge)[kShift ? 32 * NV : 1], LoadH h, LoadY y, LoadGate gate,
@@ -424,7 +458,7 @@ __device__ __forceinline__ void norm_token(const Cut<kShift>& cut, const NormPar
 #pragma unroll
       for (int u = 0; u < 4; ++u) v[i][u] = get2(r, u);
     }
-    if (post_weight) norm_apply<NV>(v, norm_statistic<NV, kShift>(cut, v, p, red), post_weight, post_bias);
+    if (post_weight) norm_apply<NV>(v, norm_statistic<kLayer, NV, kShift>(cut, v, p, red), post_weight, post_bias);
     if (p.gate) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -450,7 +484,7 @@ __device__ __forceinline__ void norm_token(const Cut<kShift>& cut, const NormPar
   clear_past<NV, kShift>(cut, v, d);
   if (p.h_out) store_row<NV, kShift>(cut, (H*)p.h_out + t * p.ldh_out, v, d);
   if (!p.weight) return;
-  const float r = norm_statistic<NV, kShift>(cut, v, p, red);
+  const float r = norm_statistic<kLayer, NV, kShift>(cut, v, p, red);
   release();
   norm_apply<NV>(v, r, weight, bias);
   if (p.x) store_row<NV, kShift>(cut, (T*)p.x + t * p.ldx, v, d);
@@ -473,9 +507,9 @@ __device__ __forceinline__ void norm_token(const Cut<kShift>& cut, const NormPar
 // overlap the others'.  One token of 4096 takes 2.3 us, all latency; 8192 of
 // them with both norms and a gate 57, bound by memory that reads and writes in
 // turn (the bytes alone 42).
-template <typename T, typename H, int NV, bool kShift>
+template <bool kLayer, typename T, typename H, int NV, bool kShift>
 __global__ void __launch_bounds__(1024) norm_tokens_kernel(const __grid_constant__ NormParams p) {
-  __shared__ uint32_t buf[64];
+  __shared__ __align__(8) uint32_t buf[kExchange];
   __shared__ uint64_t edge[kShift ? 32 * NV : 1];
   const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= p.tokens) return;
@@ -498,7 +532,7 @@ __global__ void __launch_bounds__(1024) norm_tokens_kernel(const __grid_constant
   const V gate(cut, gr, d);
   const V post_weight(cut, p.post_weight, d), post_bias(cut, p.post_bias, d);
   const V weight(cut, p.weight, d), bias(cut, p.bias, d);
-  norm_token<T, H, NV, kShift>(
+  norm_token<kLayer, T, H, NV, kShift>(
       cut, p, t, red, edge, [&](int i) { return h[i]; }, [&](int i) { return y[i]; }, [&](int i) { return gate.chunk(i); },
       post_weight, post_bias, weight, bias, [] {});
 }
@@ -595,7 +629,7 @@ __global__ void __launch_bounds__(1024) quantize_stream_kernel(const T* __restri
                                                                float* __restrict__ scale, int32_t* __restrict__ sum,
                                                                int stages, int stage_bytes, uint32_t* status) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint32_t buf[64];
+  __shared__ __align__(8) uint32_t buf[kExchange];
   __shared__ uint64_t full[kMaxStages];
   grid_launch_dependents();
   const int step = 8 * (int)blockDim.x;
@@ -649,12 +683,12 @@ __global__ void __launch_bounds__(1024) quantize_stream_kernel(const T* __restri
 // left the instruction cache; and in loops over shared memory the weights had
 // to come from L2 for every row, where here they stay in registers for all of
 // a block's rows.
-template <typename T, typename H, bool kShift, int MaxThreads>
+template <bool kLayer, typename T, typename H, bool kShift, int MaxThreads>
 __global__ void __launch_bounds__(MaxThreads, 1) norm_stream_kernel(const __grid_constant__ NormParams p) {
   constexpr int NV = kStreamChunks;
   using V = Vector<T, NV, true, kShift>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint32_t buf[64];
+  __shared__ __align__(8) uint32_t buf[kExchange];
   __shared__ uint64_t edge[kShift ? 32 * NV : 1];
   __shared__ uint64_t full[kMaxStages];
   const int d = p.d, stages = p.stages;
@@ -693,7 +727,7 @@ __global__ void __launch_bounds__(MaxThreads, 1) norm_stream_kernel(const __grid
     }
     const H* const hr = h.at(stage, t);
     const T *const yr = y.at(stage + y_at, t), *const gr = g.at(stage + g_at, t);
-    norm_token<T, H, NV, kShift>(
+    norm_token<kLayer, T, H, NV, kShift>(
         cut, p, t, red, edge, [&](int i) { return load_chunk<kShift>(cut, hr, cut.start(i), d); },
         [&](int i) { return load_chunk<kShift>(cut, yr, cut.start(i), d); },
         [&](int i) { return gates ? load_chunk<kShift>(cut, gr, cut.start(i), d) : gate.chunk(i); }, post_weight,
@@ -848,10 +882,10 @@ cudaError_t launch_quantize(const T* X, int64_t tokens, int d, int64_t ldx, int8
   return cudaGetLastError();
 }
 
-template <typename T, typename H, bool kShift, int MaxThreads>
+template <bool kLayer, typename T, typename H, bool kShift, int MaxThreads>
 cudaError_t launch_stream(const NormParams& p, const StreamShape& shape, int bias_bytes, cudaStream_t st) {
   const int smem = p.stages * p.stage_bytes + bias_bytes;
-  const auto kernel = norm_stream_kernel<T, H, kShift, MaxThreads>;
+  const auto kernel = norm_stream_kernel<kLayer, T, H, kShift, MaxThreads>;
   const cudaError_t e = ensure_smem_limit((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
   kernel<<<stream_grid(p.tokens, shape.blocks, kShift), shape.threads, smem, st>>>(p);
@@ -859,20 +893,20 @@ cudaError_t launch_stream(const NormParams& p, const StreamShape& shape, int bia
   return cudaGetLastError();
 }
 
-template <typename T, typename H, int NV>
+template <bool kLayer, typename T, typename H, int NV>
 cudaError_t launch_rows(const NormParams& p, cudaStream_t st) {
   const dim3 block = row_block(span(p.d, !p.aligned), NV);
   const unsigned grid = (unsigned)((p.tokens + block.y - 1) / block.y);
   if (p.aligned)
-    norm_tokens_kernel<T, H, NV, false><<<grid, block, 0, st>>>(p);
+    norm_tokens_kernel<kLayer, T, H, NV, false><<<grid, block, 0, st>>>(p);
   else
-    norm_tokens_kernel<T, H, NV, true><<<grid, block, 0, st>>>(p);
+    norm_tokens_kernel<kLayer, T, H, NV, true><<<grid, block, 0, st>>>(p);
   note_launch();
   return cudaGetLastError();
 }
 
-template <typename T, typename H>
-cudaError_t launch_norm(NormParams& p, cudaStream_t st) {
+template <bool kLayer, typename T, typename H>
+cudaError_t launch_norm_kind(NormParams& p, cudaStream_t st) {
   const int sms = device_info().sms;
   const bool whole = p.aligned && p.d % 8 == 0;
   if (p.weight && span(p.d, !whole) <= 1024 * 8 * kStreamChunks && streams_norm(p.d, p.tokens, sms)) {
@@ -896,14 +930,21 @@ cudaError_t launch_norm(NormParams& p, cudaStream_t st) {
     // 768 threads leave each 85 registers, which the vectors need; wider rows
     // have to do with 64
     if (p.stages && whole)
-      return shape.threads <= 768 ? launch_stream<T, H, false, 768>(p, shape, bias_bytes, st)
-                                  : launch_stream<T, H, false, 1024>(p, shape, bias_bytes, st);
+      return shape.threads <= 768 ? launch_stream<kLayer, T, H, false, 768>(p, shape, bias_bytes, st)
+                                  : launch_stream<kLayer, T, H, false, 1024>(p, shape, bias_bytes, st);
     if (p.stages)
-      return shape.threads <= 768 ? launch_stream<T, H, true, 768>(p, shape, bias_bytes, st)
-                                  : launch_stream<T, H, true, 1024>(p, shape, bias_bytes, st);
+      return shape.threads <= 768 ? launch_stream<kLayer, T, H, true, 768>(p, shape, bias_bytes, st)
+                                  : launch_stream<kLayer, T, H, true, 1024>(p, shape, bias_bytes, st);
   }
   const int nv = row_chunks(span(p.d, !p.aligned), p.tokens, sms);
-  return nv == 1 ? launch_rows<T, H, 1>(p, st) : nv == 2 ? launch_rows<T, H, 2>(p, st) : launch_rows<T, H, 4>(p, st);
+  return nv == 1   ? launch_rows<kLayer, T, H, 1>(p, st)
+         : nv == 2 ? launch_rows<kLayer, T, H, 2>(p, st)
+                   : launch_rows<kLayer, T, H, 4>(p, st);
+}
+
+template <typename T, typename H>
+cudaError_t launch_norm(NormParams& p, bool layer, cudaStream_t st) {
+  return layer ? launch_norm_kind<true, T, H>(p, st) : launch_norm_kind<false, T, H>(p, st);
 }
 
 bool aligned_rows(const void* p, int64_t ld, gptq_dtype_t t) {  // NULL: it is not read
@@ -961,19 +1002,19 @@ gptq_status_t norm_tokens(const gptq_norm_t* a, cudaStream_t st) {
   p.alpha = a->alpha;
   p.beta = a->beta;
   p.eps = a->eps;
-  p.layer = a->kind == GPTQ_NORM_LAYER;
+  const bool layer = a->kind == GPTQ_NORM_LAYER;
   p.aligned = aligned_rows(a->h, a->ldh, a->ht) && aligned_rows(a->y, a->ldy, a->yt) &&
               aligned_rows(a->post_weight, 0, a->yt) && aligned_rows(a->post_bias, 0, a->yt) &&
               aligned_rows(a->gate, a->ldgate, a->yt) && aligned_rows(a->weight, 0, a->yt) &&
               aligned_rows(a->bias, 0, a->yt) && aligned_rows(a->h_out, a->ldh_out, a->ht) &&
               aligned_rows(a->x, a->ldx, a->yt);
   if (a->yt == GPTQ_F16)
-    CUDA_TRY((a->ht == GPTQ_F32 ? launch_norm<__half, float>(p, st) : launch_norm<__half, __half>(p, st)));
+    CUDA_TRY((a->ht == GPTQ_F32 ? launch_norm<__half, float>(p, layer, st) : launch_norm<__half, __half>(p, layer, st)));
   else if (a->yt == GPTQ_BF16)
-    CUDA_TRY((a->ht == GPTQ_F32 ? launch_norm<__nv_bfloat16, float>(p, st)
-                                : launch_norm<__nv_bfloat16, __nv_bfloat16>(p, st)));
+    CUDA_TRY((a->ht == GPTQ_F32 ? launch_norm<__nv_bfloat16, float>(p, layer, st)
+                                : launch_norm<__nv_bfloat16, __nv_bfloat16>(p, layer, st)));
   else
-    CUDA_TRY((launch_norm<float, float>(p, st)));
+    CUDA_TRY((launch_norm<float, float>(p, layer, st)));
   return GPTQ_OK;
 }
 

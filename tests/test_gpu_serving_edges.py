@@ -85,3 +85,43 @@ def test_gelu_keeps_its_relative_accuracy_where_it_vanishes(lib, tokens, dtype):
     # (Mills' ratio) and 2 above.  erfcf is within 4 units of 2^-23 (documented); 6 roundings around it.
     tol = want.abs() * ((g ** 2 + 3) * 4 * R.U32 + 4 * 2.0 ** -23 + 6 * R.U32 + R.U[dtype]) * 1.01 + R.FLOOR[dtype]
     _within(y, want, tol)
+
+
+# ----------------------------------------------- layer norms far from their mean
+ROWS = [(1, 4096), (3, 77), (200, 264), (5, 11008), (700, 9000), (650, 9001), (1500, 4096), (700, 4001), (3, 20000)]
+
+
+@pytest.mark.parametrize("tokens,d", ROWS)
+@pytest.mark.parametrize("spread", [0.0, 0.05])
+def test_layer_norm_of_rows_with_a_large_common_offset(lib, tokens, d, spread):
+    """fp32 rows around +-1000, all equal or 1/20000 of that apart, as h and, with
+    a post-norm, as y."""
+    rng = np.random.default_rng([23, tokens, d])
+    base = 1000.1 * np.where(np.arange(tokens) % 2, -1, 1)[:, None] * (1 + 0.01 * rng.random((tokens, 1)))
+    v = (base + spread * rng.standard_normal((tokens, d))).astype(np.float32)
+    w, b = (1 + 0.2 * rng.standard_normal(d)).astype(np.float32), rng.standard_normal(d).astype(np.float32)
+    dev = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    eps = float(np.float32(1e-5))
+    a = v.astype(np.float64)
+    mean = a.mean(1, keepdims=True)
+    c = a - mean
+    r = 1 / np.sqrt((c ** 2).mean(1, keepdims=True) + eps)
+    x = c * r * w
+    # A first mean is off by no more than R.ROUNDINGS roundings of its size, and
+    # so are the values without it; their sum takes that out again, but for
+    # R.ROUNDINGS roundings of what it sums.
+    n = R.ROUNDINGS * R.U32
+    size = np.abs(c).mean(1, keepdims=True) + n * np.abs(mean)
+    dv = R.U32 * (np.abs(c) + n * np.abs(mean)) + n * size
+    # the variance: its own sum's roundings, and those of the squared residue taken from it
+    dr = 1.5 * n * r ** 2 * ((c ** 2).mean(1, keepdims=True) + (n * mean) ** 2)
+    tol = (dv * r * np.abs(w) + np.abs(x) * (dr + 4 * R.U32) + R.U32 * np.abs(x + b) * 2) * 1.05
+    got, out = lib.norm_tokens(dev(v), None, dev(w), bias=dev(b), kind="layer", eps=eps)
+    want = torch.from_numpy(x + b).cuda()
+    _within(out, want, torch.from_numpy(tol).cuda())
+    h1, _ = lib.norm_tokens(torch.zeros_like(got), dev(v), dev(w), bias=dev(b), post_weight=dev(w), post_bias=dev(b),
+                            kind="layer", eps=eps)
+    _within(h1, want, torch.from_numpy(tol).cuda())
+    _, t = lib.norm_tokens(dev(v), None, dev(w), bias=dev(b), kind="layer", eps=eps, quantize=True)
+    half = (0.5 + 1e-4) * t.scale.double()[:, None]
+    _within(t.q.double() * t.scale.double()[:, None], want, half + torch.from_numpy(tol).cuda())
