@@ -125,6 +125,16 @@ struct On {
   }
 };
 
+// The interpreter is free for other threads: a launch may wait for room in a
+// full queue and an allocation for the device, and a host callback that the
+// stream has yet to run may need the interpreter.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 at::Tensor empty(at::IntArrayRef size, at::ScalarType type, const at::Device& device) {
   return at::empty(size, at::TensorOptions().dtype(type).device(device));
 }
@@ -179,19 +189,25 @@ at::Tensor product(PyObject* x, PyObject* w, PyObject* up, PyObject* bias, int a
                                                : X.scalar_type();
   const gptq_dtype_t yt = code(type);
   On on(device);
-  at::Tensor Y = empty({T, out}, type, device);
-  if (tokens8) {
-    check(up ? gptq_matmul_int8_gated(&q, T, in, &lw, &lu, out, (gptq_act_t)act, Y.data_ptr(), yt, out, on.stream)
-             : gptq_matmul_int8(&q, T, in, &lw, out, b, Y.data_ptr(), yt, out, on.stream));
-    return Y;
+  at::Tensor Y, ws;
+  gptq_status_t status;
+  {
+    Unlocked unlocked;
+    Y = empty({T, out}, type, device);
+    void* const y = Y.data_ptr();
+    if (tokens8) {
+      status = up ? gptq_matmul_int8_gated(&q, T, in, &lw, &lu, out, (gptq_act_t)act, y, yt, out, on.stream)
+                  : gptq_matmul_int8(&q, T, in, &lw, out, b, y, yt, out, on.stream);
+    } else {
+      const size_t n = gptq_linear_int8_ws_bytes(T, in);
+      if (n) ws = empty({(int64_t)n}, at::kByte, device);
+      void* const wsp = n ? ws.data_ptr() : nullptr;
+      status = up ? gptq_linear_int8_gated(X.data_ptr(), xt, T, in, ldx, &lw, &lu, out, (gptq_act_t)act, y, yt, out, wsp,
+                                           n, on.stream)
+                  : gptq_linear_int8(X.data_ptr(), xt, T, in, ldx, &lw, out, b, y, yt, out, wsp, n, on.stream);
+    }
   }
-  const size_t n = gptq_linear_int8_ws_bytes(T, in);
-  at::Tensor ws;
-  if (n) ws = empty({(int64_t)n}, at::kByte, device);
-  void* wsp = n ? ws.data_ptr() : nullptr;
-  check(up ? gptq_linear_int8_gated(X.data_ptr(), xt, T, in, ldx, &lw, &lu, out, (gptq_act_t)act, Y.data_ptr(), yt, out,
-                                    wsp, n, on.stream)
-           : gptq_linear_int8(X.data_ptr(), xt, T, in, ldx, &lw, out, b, Y.data_ptr(), yt, out, wsp, n, on.stream));
+  check(status);
   return Y;
 }
 
@@ -245,10 +261,16 @@ PyObject* py_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t ld = row_stride(X, "X");
     const gptq_dtype_t xt = code(X.scalar_type());
     On on(X.device());
-    const NewTokens x(X.size(0), X.size(1), X.device());
-    check(gptq_quantize_tokens(X.data_ptr(), xt, X.size(0), X.size(1), ld, (int8_t*)x.q.data_ptr(), x.ld,
-                               (float*)x.scale.data_ptr(), (int32_t*)x.sum.data_ptr(), on.stream));
-    return x.wrap();
+    std::optional<NewTokens> x;
+    gptq_status_t status;
+    {
+      Unlocked unlocked;
+      x.emplace(X.size(0), X.size(1), X.device());
+      status = gptq_quantize_tokens(X.data_ptr(), xt, X.size(0), X.size(1), ld, (int8_t*)x->q.data_ptr(), x->ld,
+                                    (float*)x->scale.data_ptr(), (int32_t*)x->sum.data_ptr(), on.stream);
+    }
+    check(status);
+    return x->wrap();
   });
 }
 
@@ -295,27 +317,32 @@ PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const bool quantize = PyObject_IsTrue(a[11]) == 1, inplace = PyObject_IsTrue(a[12]) == 1;
     On on(device);
     at::Tensor h_out, x;
-    if (inplace) {
-      p.h_out = h.data_ptr();
-      p.ldh_out = p.ldh;
-    } else if (a[1] != Py_None || alpha != 1.0) {
-      h_out = empty({T, d}, ht, device);
-      p.h_out = h_out.data_ptr();
-      p.ldh_out = d;
-    }
     std::optional<NewTokens> tokens;
-    if (quantize) {
-      tokens.emplace(T, d, device);
-      p.q = (int8_t*)tokens->q.data_ptr();
-      p.ldq = tokens->ld;
-      p.scale = (float*)tokens->scale.data_ptr();
-      p.sum = (int32_t*)tokens->sum.data_ptr();
-    } else {
-      x = empty({T, d}, yt, device);
-      p.x = x.data_ptr();
-      p.ldx = d;
+    gptq_status_t status;
+    {
+      Unlocked unlocked;
+      if (inplace) {
+        p.h_out = h.data_ptr();
+        p.ldh_out = p.ldh;
+      } else if (a[1] != Py_None || alpha != 1.0) {
+        h_out = empty({T, d}, ht, device);
+        p.h_out = h_out.data_ptr();
+        p.ldh_out = d;
+      }
+      if (quantize) {
+        tokens.emplace(T, d, device);
+        p.q = (int8_t*)tokens->q.data_ptr();
+        p.ldq = tokens->ld;
+        p.scale = (float*)tokens->scale.data_ptr();
+        p.sum = (int32_t*)tokens->sum.data_ptr();
+      } else {
+        x = empty({T, d}, yt, device);
+        p.x = x.data_ptr();
+        p.ldx = d;
+      }
+      status = gptq_norm_tokens(&p, on.stream);
     }
-    check(gptq_norm_tokens(&p, on.stream));
+    check(status);
     PyObject* second = quantize ? tokens->wrap() : THPVariable_Wrap(x);
     if (!second) return nullptr;
     PyObject* first = h_out.defined() ? THPVariable_Wrap(h_out) : (Py_INCREF(a[0]), a[0]);

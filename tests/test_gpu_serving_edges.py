@@ -125,3 +125,66 @@ def test_layer_norm_of_rows_with_a_large_common_offset(lib, tokens, d, spread):
     _, t = lib.norm_tokens(dev(v), None, dev(w), bias=dev(b), kind="layer", eps=eps, quantize=True)
     half = (0.5 + 1e-4) * t.scale.double()[:, None]
     _within(t.q.double() * t.scale.double()[:, None], want, half + torch.from_numpy(tol).cuda())
+
+
+# ------------------------------------------------------------- other host threads
+_STUB = r"""
+#include <time.h>
+static volatile int other_ran = 0;
+void let_go(void) { other_ran = 1; }
+void again(void) { other_ran = 0; }
+static int wait_for_other(void) {  /* GPTQ_OK once another thread has run, GPTQ_ERR_TIMEOUT after two seconds */
+  struct timespec t = {0, 1000000};
+  for (int i = 0; i < 2000 && !other_ran; ++i) nanosleep(&t, 0);
+  return other_ran ? 0 : 6;
+}
+int gptq_quantize_tokens() { return wait_for_other(); }
+int gptq_norm_tokens() { return wait_for_other(); }
+int gptq_matmul_int8() { return wait_for_other(); }
+int gptq_matmul_int8_gated() { return wait_for_other(); }
+int gptq_linear_int8() { return wait_for_other(); }
+int gptq_linear_int8_gated() { return wait_for_other(); }
+"""
+
+_THREADS = r"""
+import ctypes, sys, threading, time
+import torch, post_weight_quantization_13_b200 as g
+stub = ctypes.CDLL(sys.argv[1])
+x = torch.ones(40, 64, device='cuda', dtype=torch.bfloat16)
+w = torch.ones(64, device='cuda', dtype=torch.bfloat16)
+layer = g.Int8Layer(torch.ones(64, 64, device='cuda', dtype=torch.int8), torch.ones(64, device='cuda'))
+t = g.Int8Tokens(layer.weight, layer.scale, layer.scale.int())
+calls = {'quantize': lambda: g.quantize_tokens(x), 'norm': lambda: g.norm_tokens(x, x, w),
+         'linear': lambda: g.linear_int8(x, layer), 'gated': lambda: g.gated_int8(x, layer, layer),
+         'linear, tokens': lambda: g.linear_int8(t, layer), 'gated, tokens': lambda: g.gated_int8(t, layer, layer)}
+stuck = []
+for name, call in calls.items():
+    stub.again()
+    def other():
+        time.sleep(0.1)
+        stub.let_go()
+    th = threading.Thread(target=other)
+    th.start()
+    try:
+        call()
+    except g.GptqError as e:
+        stuck.append(name)
+    th.join()
+assert not stuck, stuck
+"""
+
+
+def test_other_threads_run_while_a_call_is_in_the_library(tmp_path):
+    """A launch can wait for room in a full queue; a host callback ahead of it may
+    need the interpreter.  The library is replaced by calls that wait for another
+    Python thread."""
+    import os
+    import subprocess
+    import sys
+    (tmp_path / "stub.c").write_text(_STUB)
+    stub = str(tmp_path / "stub.so")
+    subprocess.run(["gcc", "-shared", "-fPIC", "-O1", "-w", "-o", stub, str(tmp_path / "stub.c")], check=True)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _THREADS, stub], cwd=root, capture_output=True, text=True, timeout=300,
+                       env={**os.environ, "LD_PRELOAD": stub})
+    assert r.returncode == 0, r.stderr[-2000:]
