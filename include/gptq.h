@@ -601,9 +601,18 @@ gptq_status_t gptq_linear_int8_gated(const void* X, gptq_dtype_t xt,
  * Waits for stream and returns GPTQ_ERR_TIMEOUT if a bounded device-side wait
  * in any of these calls on the current device has given up since the last such
  * call (the results concerned are incomplete), else GPTQ_OK.  Clears the
- * status.
+ * status it reports: a wait that gives up on another stream meanwhile is
+ * reported by this call or by a later one.
  */
 gptq_status_t gptq_int8_status(void* stream);
+
+/*
+ * Diagnostic: runs that path on purpose.  Enqueues a kernel that waits on a
+ * barrier which nothing completes, as the serving kernels wait, gives up after
+ * limit_ns nanoseconds (1 .. 2e9) and raises their status, so the next
+ * gptq_int8_status returns GPTQ_ERR_TIMEOUT.  The device stays usable.
+ */
+gptq_status_t gptq_selftest_int8_timeout(uint64_t limit_ns, void* stream);
 
 #ifdef __cplusplus
 }

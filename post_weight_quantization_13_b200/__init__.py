@@ -27,7 +27,7 @@ __all__ = [
     "gptq_quantize_layer", "gptq_quantize_layer_noalloc", "GPTQ_STATIC_SCRATCH_BYTES",
     "gptq_workspace_status", "gptq_quantize_layer_noalloc_status",
     "gptq_dequantize_layer", "gptq_export_checkpoint", "gptq_selftest_wait_timeout",
-    "gptq_selftest_quotient",
+    "gptq_selftest_quotient", "gptq_selftest_int8_timeout",
     "solve_layer", "solve_block", "export_checkpoint", "STATUS_NAMES",
     "gptq_layout_int8", "gptq_quantize_tokens", "gptq_norm_tokens", "gptq_matmul_int8",
     "gptq_matmul_int8_gated", "gptq_linear_int8", "gptq_linear_int8_gated",
@@ -96,6 +96,8 @@ lib.gptq_export_checkpoint.restype = ctypes.c_int
 
 lib.gptq_selftest_wait_timeout.argtypes = [ctypes.c_uint64, _p]
 lib.gptq_selftest_wait_timeout.restype = ctypes.c_int
+lib.gptq_selftest_int8_timeout.argtypes = [ctypes.c_uint64, _p]
+lib.gptq_selftest_int8_timeout.restype = ctypes.c_int
 lib.gptq_selftest_quotient.argtypes = [ctypes.c_uint64, ctypes.c_uint64, ctypes.POINTER(ctypes.c_uint64),
                                        ctypes.POINTER(ctypes.c_uint64), _p]
 lib.gptq_selftest_quotient.restype = ctypes.c_int
@@ -270,6 +272,12 @@ def gptq_selftest_wait_timeout(limit_ns: int, stream=None) -> int:
     """Run the bounded-wait timeout path once; returns the status code
     (GPTQ_ERR_TIMEOUT = 6 when the path works)."""
     return lib.gptq_selftest_wait_timeout(int(limit_ns), _stream(stream))
+
+
+def gptq_selftest_int8_timeout(limit_ns: int, stream=None) -> None:
+    """Enqueue a kernel whose bounded wait gives up after limit_ns, as a serving
+    kernel's would; the next gptq_int8_status raises GptqError."""
+    _check(lib.gptq_selftest_int8_timeout(int(limit_ns), _stream(stream)))
 
 
 def solve_layer(W, X=None, cfg=None, S=None, n=None, with_codes=True, stream=None):

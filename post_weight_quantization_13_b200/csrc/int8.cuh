@@ -171,7 +171,7 @@ __device__ __forceinline__ uint32_t elect_lane() {
   return leader;
 }
 // As mbar_wait, false once the limit is past.
-__device__ __forceinline__ bool wait_at(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_at(uint32_t bar, uint32_t parity, uint64_t limit_ns = kWaitLimitNs) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -182,7 +182,7 @@ __device__ __forceinline__ bool wait_at(uint32_t bar, uint32_t parity) {
       : "memory");
   if (ok) return true;
   const uint64_t start = globaltimer();
-  while (globaltimer() - start <= kWaitLimitNs) {
+  while (globaltimer() - start <= limit_ns) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"

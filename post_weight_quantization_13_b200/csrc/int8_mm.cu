@@ -638,6 +638,8 @@ gptq_status_t int8_status(cudaStream_t st) {
   uint32_t* at = nullptr;
   CUDA_TRY(int8_status_word(&at));
   CUDA_TRY(cudaMemcpyAsync(&status, at, sizeof(status), cudaMemcpyDeviceToHost, st));
+  CUDA_TRY(cudaStreamSynchronize(st));
+  if (status == 0) return GPTQ_OK;  // and nothing to clear: a flag that another stream raises by now stays
   CUDA_TRY(cudaMemsetAsync(at, 0, sizeof(status), st));
   CUDA_TRY(cudaStreamSynchronize(st));
   if (status & ST_TIMEOUT) return fail(GPTQ_ERR_TIMEOUT, "a bounded device-side wait gave up in an int8 kernel");

@@ -3,6 +3,10 @@
 // ever arrives on; the wait gives up after limit_ns of %globaltimer and
 // raises the timeout flag in a status word, which the host then reads.  No
 // fault, trap or unbounded spin is involved, and the context stays usable.
+//
+// gptq_selftest_int8_timeout: the same with the 8-bit serving kernels' wait and
+// their status word, which gptq_int8_status then reads.
+#include "int8.cuh"
 #include "internal.cuh"
 
 namespace gptq {
@@ -27,6 +31,16 @@ __global__ void selftest_wait_kernel(uint64_t limit_ns) {
     }
     if (done) atomicOr(&g_selftest_status, ST_TIMEOUT);
   }
+}
+
+__global__ void selftest_int8_wait_kernel(uint64_t limit_ns, uint32_t* status) {
+  __shared__ uint64_t bar;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (!wait_at(smem_u32(&bar), 0, limit_ns) && threadIdx.x == 0) raise_status(status, ST_TIMEOUT);
 }
 
 __device__ unsigned long long g_quot_count[2];  // pairs checked, mismatches
@@ -92,6 +106,21 @@ extern "C" gptq_status_t gptq_selftest_quotient(uint64_t n, uint64_t seed, uint6
   CUDA_TRY(cudaStreamSynchronize(st));
   *checked = c[0];
   *mismatches = c[1];
+  return GPTQ_OK;
+}
+
+extern "C" gptq_status_t gptq_selftest_int8_timeout(uint64_t limit_ns, void* stream) {
+  using namespace gptq;
+  clear_error();
+  if (limit_ns == 0 || limit_ns > kWaitLimitNs)
+    return fail(GPTQ_ERR_INVALID_ARG, "limit_ns must be in [1, %llu]", (unsigned long long)kWaitLimitNs);
+  const gptq_status_t s = check_device();
+  if (s != GPTQ_OK) return s;
+  uint32_t* status = nullptr;
+  CUDA_TRY(int8_status_word(&status));
+  selftest_int8_wait_kernel<<<1, 32, 0, (cudaStream_t)stream>>>(limit_ns, status);
+  note_launch();
+  CUDA_TRY(cudaGetLastError());
   return GPTQ_OK;
 }
 

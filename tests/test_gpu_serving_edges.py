@@ -188,3 +188,44 @@ def test_other_threads_run_while_a_call_is_in_the_library(tmp_path):
     r = subprocess.run([sys.executable, "-c", _THREADS, stub], cwd=root, capture_output=True, text=True, timeout=300,
                        env={**os.environ, "LD_PRELOAD": stub})
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+# ------------------------------------------------------------ waits that give up
+def _gave_up(lib, stream=None):
+    try:
+        lib.gptq_int8_status(stream)
+    except lib.GptqError as e:
+        assert e.status == 6 and "gave up" in str(e)
+        return True
+    return False
+
+
+def test_a_wait_that_gives_up_is_reported_once(lib):
+    lib.gptq_int8_status()
+    lib.gptq_selftest_int8_timeout(200_000)
+    assert _gave_up(lib)
+    assert not _gave_up(lib)
+    rng = np.random.default_rng(31)                 # the device is as usable as before
+    layer = R.random_layer(rng, 40, 64)
+    x = torch.from_numpy(rng.standard_normal((5, 64)).astype(np.float32))
+    q, s = R.quantize(x.numpy())
+    p = R.product(q, s, layer)
+    _within(lib.linear_int8(x.cuda(), R.on_device(lib, layer)).cpu(), torch.from_numpy(p),
+            torch.from_numpy(R.linear_tol(p, None, F32)))
+    assert not _gave_up(lib)
+
+
+def test_reports_from_another_stream_are_not_lost(lib):
+    """A wait gives up on one stream while the status is read on another, again
+    and again: it is reported by a reading that was under way, or by the next."""
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    lib.gptq_int8_status()
+    done = torch.cuda.Event()
+    for i in range(1000):
+        lib.gptq_selftest_int8_timeout(1000 + 37 * i, a)
+        done.record(a)
+        reported = 0
+        while not done.query():
+            reported += _gave_up(lib, b)
+        reported += _gave_up(lib, a)
+        assert reported, i

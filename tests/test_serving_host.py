@@ -268,3 +268,9 @@ def test_serving_names_are_public(g):
         assert name in g.__all__ and callable(getattr(g, name))
     with pytest.raises(AttributeError):
         g.no_such_call
+
+
+def test_int8_timeout_selftest_refuses_bad_limits(g):
+    for limit in (0, 3 * 10 ** 9):
+        assert g.lib.gptq_selftest_int8_timeout(limit, None) == INVALID
+        assert "limit_ns" in g.gptq_last_error()
