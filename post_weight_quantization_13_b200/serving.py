@@ -23,7 +23,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import GptqError, _check, _i64, _p, _stream, lib
+from . import GptqError, _check, _i64, _p, lib
 from . import _serving  # type: ignore[attr-defined]  (built beside libgptq.so; there is no fallback)
 
 _NORMS = {"rms": 0, "layer": 1}
@@ -303,8 +303,10 @@ def _workspace(ws, dev):
 
 def gptq_int8_status(stream=None) -> None:
     """Wait for the stream and raise GptqError if a bounded device-side wait
-    of any of these calls on this device has given up since the last time."""
-    _check(lib.gptq_int8_status(_stream(stream)))
+    of any of these calls on its device has given up since the last time.
+    The calls themselves do not wait for the device and cannot tell."""
+    _call(torch.device("cuda", torch.cuda.current_device()) if stream is None else stream.device, stream,
+          lib.gptq_int8_status)
 
 
 # ---------------------------------------------------------- allocating calls

@@ -274,3 +274,30 @@ def test_int8_timeout_selftest_refuses_bad_limits(g):
     for limit in (0, 3 * 10 ** 9):
         assert g.lib.gptq_selftest_int8_timeout(limit, None) == INVALID
         assert "limit_ns" in g.gptq_last_error()
+
+
+def test_int8_status_is_that_of_the_streams_device(g, S, monkeypatch):
+    """A stream of another device than the current one: two devices that answer
+    by themselves."""
+    import contextlib
+    import types
+    current, asked = [0], []
+
+    @contextlib.contextmanager
+    def device(index):
+        before, current[0] = current[0], index
+        yield
+        current[0] = before
+
+    def status(raw):
+        asked.append((current[0], raw))
+        return 0
+
+    monkeypatch.setattr(S.torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(S.torch.cuda, "device", device)
+    monkeypatch.setattr(S, "_raw_stream", lambda index: 100 + index)
+    monkeypatch.setattr(S, "lib", types.SimpleNamespace(gptq_int8_status=status))
+    g.gptq_int8_status()
+    g.gptq_int8_status(types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=7))
+    g.gptq_int8_status(types.SimpleNamespace(device=torch.device("cuda", 0), cuda_stream=8))
+    assert asked == [(0, 100), (1, 7), (0, 8)] and current == [0]
