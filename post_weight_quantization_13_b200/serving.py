@@ -370,7 +370,19 @@ def mlp_int8(h, y, weight, gate, up, down, act="silu", **norm):
     """The MLP half of a solved decoder block: (h', z) with h' the residual
     stream after the attention output y and z = down(act(gate x) * up x), x
     the pre-norm of h'.  ``norm`` takes norm_tokens' keywords.  Feed (h', z)
-    to the next block's norm_tokens."""
+    to the next block's norm_tokens.  Refused layers leave h as it was."""
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    if norm.get("inplace"):     # the products' own checks come when h is overwritten
+        d = h.shape[-1]
+        _, _, inter, _ = _c_pair(gate, up, d, h.device, act)
+        _c_layer(down, inter, h.device, "down")
+        for name, layer, in_ in (("gate", gate, d), ("up", up, d), ("down", down, inter)):
+            w = layer[0]
+            if w.data_ptr() % 16 or (w.shape[0] > 1 and (w.stride(0) % 16 or w.stride(0) < in_)):
+                raise ValueError(f"{name}.weight must have rows on 16-byte boundaries")
+            if not 1 <= in_ <= 32768 or w.shape[0] > 65535:
+                raise ValueError(f"{name}: {w.shape[0]} x {in_} exceeds 65535 x 32768")
     h, x = norm_tokens(h, y, weight, quantize=True, **norm)
     a = gated_int8(x, gate, up, act, dtype=weight.dtype)
     return h, linear_int8(a, down)

@@ -301,3 +301,27 @@ def test_int8_status_is_that_of_the_streams_device(g, S, monkeypatch):
     g.gptq_int8_status(types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=7))
     g.gptq_int8_status(types.SimpleNamespace(device=torch.device("cuda", 0), cuda_stream=8))
     assert asked == [(0, 100), (1, 7), (0, 8)] and current == [0]
+
+
+def test_mlp_refuses_before_it_overwrites_the_residual_stream(g, S, monkeypatch):
+    def overwritten(*a, **k):
+        raise AssertionError("the norm ran")
+
+    monkeypatch.setattr(S, "norm_tokens", overwritten)
+    h, w = torch.ones(4, 64), torch.ones(64)
+
+    def layer(out, in_, pad=0):
+        return g.Int8Layer(torch.zeros(out, in_ + pad, dtype=torch.int8)[:, :in_], torch.ones(out))
+
+    gate, down = layer(96, 64), layer(64, 96)
+    for a in ((gate, gate, down, "relu"), (layer(96, 48), gate, down, "silu"), (gate, layer(80, 64), down, "silu"),
+              (gate, gate, layer(64, 80), "silu"), (gate, gate._replace(scale=torch.ones(5)), down, "silu"),
+              (gate, gate, down._replace(weight=down.weight.int()), "silu"), (gate, layer(96, 64, 8), down, "gelu"),
+              (gate, gate, layer(64, 96)._replace(zero=torch.zeros(64)), "silu"),
+              (layer(3, 65536, 0), layer(3, 65536, 0), layer(65536, 3, 13), "silu")):
+        with pytest.raises(ValueError):
+            g.mlp_int8(h, h, w, *a, inplace=True)
+    with pytest.raises(ValueError):
+        g.mlp_int8(h, h, w, gate, gate, down, "relu")
+    with pytest.raises(AssertionError, match="the norm ran"):
+        g.mlp_int8(h, h, w, gate, gate, down, inplace=True)
