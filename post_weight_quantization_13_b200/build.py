@@ -1,6 +1,6 @@
-"""Build libgptq.so in-tree for sm_100a with nvcc (no torch involved), and
-_serving.so, the CPython module behind serving.py's allocating calls, with g++
-against torch's headers.
+"""Build libgptq.so in-tree for sm_100a with nvcc (no torch involved), and,
+where torch is installed, _serving.so, the CPython module behind serving.py's
+allocating calls, with g++ against torch's headers.
 
     python post_weight_quantization_13_b200/build.py [--force]
 
@@ -9,15 +9,19 @@ the library this script builds)
 
 Objects go to ``post_weight_quantization_13_b200/_build/``; the shared
 libraries land next to this file.  Translation units compile in parallel and
-are rebuilt only when a source or header is newer than the library.
+are rebuilt only when a source or header is newer than the library, _serving.so
+also when it was built for another torch or Python.
 """
 from __future__ import annotations
 
 import glob
 import os
+import importlib.metadata
+import importlib.util
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -26,6 +30,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgptq.so")
 EXT = os.path.join(HERE, "_serving.so")
+EXT_FOR = os.path.join(BUILD, "_serving.for")   # the torch and Python _serving.so was built for
 EXT_SOURCE = os.path.join(CSRC, "serving_ext.cpp")
 INCLUDE = os.path.join(ROOT, "include")
 
@@ -58,12 +63,29 @@ def up_to_date() -> bool:
     return _newer(LIB, _inputs())
 
 
+def has_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
+
+
+def _ext_for() -> str:
+    try:
+        torch = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:     # on the path, but not installed as a package
+        torch = importlib.util.find_spec("torch").origin
+    return f"torch {torch}, {sysconfig.get_config_var('SOABI')}"
+
+
 def ext_up_to_date() -> bool:
-    return _newer(EXT, [EXT_SOURCE, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h")))
+    if not _newer(EXT, [EXT_SOURCE, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))):
+        return False
+    try:
+        with open(EXT_FOR) as f:
+            return f.read() == _ext_for()
+    except FileNotFoundError:
+        return False
 
 
 def build_ext(verbose: bool = False) -> str:
-    import sysconfig
     import torch
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
@@ -81,13 +103,18 @@ def build_ext(verbose: bool = False) -> str:
     if verbose:
         sys.stderr.write(r.stderr)
     os.replace(tmp, EXT)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(EXT_FOR, "w") as f:
+        f.write(_ext_for())
     return EXT
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     if force or not up_to_date():
         _build_lib(verbose, ptxas_info)
-    if force or not ext_up_to_date():
+    if not has_torch():
+        sys.stderr.write("torch is not installed: the 8-bit serving calls of the Python package are not built\n")
+    elif force or not ext_up_to_date():
         build_ext(verbose)
     return LIB
 
