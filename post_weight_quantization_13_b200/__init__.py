@@ -17,6 +17,7 @@ fails: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from dataclasses import dataclass
 
@@ -29,11 +30,16 @@ __all__ = [
     "gptq_dequantize_layer", "gptq_export_checkpoint", "gptq_selftest_wait_timeout",
     "gptq_selftest_quotient", "gptq_selftest_int8_timeout",
     "solve_layer", "solve_block", "export_checkpoint", "STATUS_NAMES",
+]
+# The serving calls (serving.py): loaded with torch at their first use.
+_SERVING = (
     "gptq_layout_int8", "gptq_quantize_tokens", "gptq_norm_tokens", "gptq_matmul_int8",
     "gptq_matmul_int8_gated", "gptq_linear_int8", "gptq_linear_int8_gated",
     "gptq_linear_int8_ws_bytes", "gptq_int8_status", "Int8Layer", "Int8Tokens", "int8_layer",
     "quantize_tokens", "norm_tokens", "linear_int8", "gated_int8", "mlp_int8",
-]
+)
+if importlib.util.find_spec("torch") is not None:   # else `import *` would fail for want of it
+    __all__ += _SERVING
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgptq.so")
 
@@ -417,9 +423,6 @@ def solve_block(layers, activations=None, cfg=None, streams=True, hessians=None)
         s_layer = r.pop("stream")
         gptq_workspace_status(ws, s_layer)
     return results
-
-
-_SERVING = frozenset(__all__[__all__.index("gptq_layout_int8"):])
 
 
 def __getattr__(name):

@@ -1,5 +1,4 @@
 """The build without torch, and for another torch than the last one's."""
-import importlib.util
 import os
 import subprocess
 import sys
@@ -34,3 +33,15 @@ def test_the_serving_module_is_built_anew_for_another_torch(build, monkeypatch):
     monkeypatch.setattr(build.importlib.metadata, "version", lambda name: "0.0")
     build.build()
     assert built == [1]
+
+
+def _python(code):
+    return subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+
+
+def test_every_name_imports_with_torch_and_the_librarys_without(build):
+    r = _python(f"from {PACKAGE} import *\nassert callable(linear_int8) and callable(solve_layer)")
+    assert r.returncode == 0, r.stderr
+    r = _python(f"import sys\nsys.modules['torch'] = None\nfrom {PACKAGE} import *\n"
+                "assert gptq_abi_version() and callable(gptq_validate_config) and 'linear_int8' not in globals()")
+    assert r.returncode == 0, r.stderr
