@@ -277,8 +277,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         vzero[i] = in && kp.wzero[g] ? __ldg(kp.wzero[g] + n) : 0;
         vbias[i] = in && biased ? __ldg(kp.bias + n) : 0.f;
       }
-      const float ts = t < kp.tokens ? __ldg(kp.tscale + t) : 0.f;
-      const int sum = t < kp.tokens ? __ldg(kp.tsum + t) : 0;
+      // (not through the read-only path: the quantizer may have written them since
+      // this kernel began)
+      const float ts = t < kp.tokens ? kp.tscale[t] : 0.f;
+      const int sum = t < kp.tokens ? kp.tsum[t] : 0;
       named_bar_sync(1, kEpilogue);
       const int buf = step & 1, use = step >> 1;
       if (!mbar_wait_sleep(&acc_full[buf], use & 1)) {

@@ -229,3 +229,27 @@ def test_reports_from_another_stream_are_not_lost(lib):
             reported += _gave_up(lib, b)
         reported += _gave_up(lib, a)
         assert reported, i
+
+
+# ------------------------------------------------ a workspace used again and again
+@pytest.mark.parametrize("tokens,in_,out", [(700, 256, 520), (3000, 512, 2048), (40, 1024, 300)])
+def test_one_workspace_for_many_calls_in_a_row(lib, tokens, in_, out):
+    """A product may begin while the quantizer ahead of it still writes the codes,
+    scales and sums of its tokens over those of the call before."""
+    rng = np.random.default_rng([37, tokens])
+    layer = R.on_device(lib, R.random_layer(rng, out, in_, True))
+    xs = [torch.from_numpy((10.0 ** (i % 5 - 2) * rng.standard_normal((tokens, in_))).astype(np.float32)).to(BF16).cuda()
+          for i in range(8)]
+    want = []
+    for x in xs:
+        t = lib.quantize_tokens(x)
+        torch.cuda.synchronize()
+        want.append(lib.linear_int8(t, layer, dtype=F32))
+    ws = torch.empty(lib.gptq_linear_int8_ws_bytes(tokens, in_), dtype=torch.uint8, device="cuda")
+    got = [torch.empty(tokens, out, device="cuda") for _ in xs]
+    for _ in range(10):
+        for y in got:
+            y.fill_(float("nan"))
+        for x, y in zip(xs, got):
+            lib.gptq_linear_int8(x, layer, y, ws)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
