@@ -253,3 +253,19 @@ def test_one_workspace_for_many_calls_in_a_row(lib, tokens, in_, out):
         for x, y in zip(xs, got):
             lib.gptq_linear_int8(x, layer, y, ws)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------- a reordered layer
+@pytest.mark.parametrize("bits", [8, 4])
+def test_int8_layer_of_a_layer_solved_in_another_order(lib, bits):
+    """desc_act: the codes stand in the weight's own order all the same."""
+    rng = np.random.default_rng([29, bits])
+    W = torch.from_numpy((0.02 * rng.standard_normal((70, 288))).astype(np.float32)).cuda()
+    X = torch.from_numpy((rng.standard_normal((288, 900)) * np.exp(rng.standard_normal((288, 1)))).astype(np.float32))
+    r = lib.solve_layer(W, X.to(F16).cuda(), dict(bits=bits, group_size=-1, sym=False, desc_act=True))
+    assert not torch.equal(r["perm"].cpu(), torch.arange(288, dtype=r["perm"].dtype))
+    layer = lib.int8_layer(r, bits)
+    deq = torch.empty(70, 288, device="cuda")
+    lib.gptq_dequantize_layer(r["qweight"], r["scales"], r["zeros"], r["g_idx"], bits, deq)
+    z = torch.zeros(70, dtype=torch.int32, device="cuda") if layer.zero is None else layer.zero
+    assert torch.equal(layer.scale[:, None] * (layer.weight.int() - z[:, None]).float(), deq)
