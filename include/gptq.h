@@ -37,8 +37,8 @@
  *     allocates device memory itself: scratch space is the caller's
  *     workspace, sized by gptq_workspace_bytes().
  *   - stream is a cudaStream_t passed as void* (NULL = the legacy default
- *     stream).  Work is enqueued on it; only gptq_prepare_hinv and
- *     gptq_selftest_wait_timeout wait for it.
+ *     stream).  Work is enqueued on it; only gptq_prepare_hinv, the status
+ *     calls, gptq_selftest_wait_timeout and gptq_selftest_quotient wait for it.
  *   - Matrices are row-major unless stated otherwise; leading dimensions are
  *     in elements.
  *   - Every call returns a gptq_status_t.  Nothing aborts or traps.  On an
@@ -429,8 +429,9 @@ gptq_status_t gptq_quantize_layer_noalloc_status(void* stream);
  *
  * All take 0 <= tokens <= 67108864 (2^26) and 1 <= in <= 32768 (here also
  * called d), work on the calling thread's current device, are asynchronous
- * on stream and keep no state between calls, so any number of them may
- * overlap on any streams and be captured into graphs.  Outputs overlap no
+ * on stream (but for gptq_int8_status) and keep no state between calls but that
+ * status, so any number of them may overlap on any streams and be captured into
+ * graphs.  Outputs overlap no
  * input and no other output unless a call says otherwise.
  * tokens == 0 and out == 0 are no-ops.  Activations are [tokens][in], tokens
  * in rows (the transpose of the Hessian's X).

@@ -2,13 +2,13 @@
 // per-token quantizer, and the norms around a block fused with its gate,
 // residual and the quantizer.
 //
-// A token's row stays in registers from its one load to its one store, so
-// every operand crosses HBM once: a thread owns NV chunks of eight
-// consecutive elements (one 16-byte load for 16-bit types), a row is owned
-// by one warp where 32 * 8 * NV elements hold it and by one block otherwise,
-// and the two or three statistics of a row (sums of squares, means, the
-// largest magnitude) are reduced by warp shuffles and one shared-memory
-// exchange each.  All statistics are fp32; a mean is subtracted before the
+// Every operand crosses HBM once.  A token's row stays in registers from its
+// one load to its one store, or, in the streaming kernels, waits for its turn in
+// shared memory: a thread owns NV chunks of eight consecutive elements (one
+// 16-byte load for 16-bit types), a row is owned by one warp where 32 * 8 * NV
+// elements hold it and by one block otherwise, and the statistics of a row (sums
+// of squares, means, the largest magnitude) are reduced by warp shuffles and one
+// shared-memory exchange each.  All statistics are fp32; a mean is subtracted before the
 // squares are summed, and what its rounding left is taken off after
 // (norm_statistic), so that rows far from zero keep their accuracy.
 #include <cuda_bf16.h>
@@ -504,9 +504,11 @@ __device__ __forceinline__ void norm_token(const Cut<kShift>& cut, const NormPar
 
 // A row a warp or a block, every operand straight to registers: few tokens, or
 // rows of which several blocks fit an SM, so that one's loads and reductions
-// overlap the others'.  One token of 4096 takes 2.3 us, all latency; 8192 of
-// them with both norms and a gate 57, bound by memory that reads and writes in
-// turn (the bytes alone 42).
+// overlap the others'.  One token of 4096 takes 2.2 us, all latency.  8000 of
+// them with one RMS norm take 42.8, the bytes alone 40.6; 8192 with both norms
+// and a gate 55 (the bytes 41.6): a second statistic for each row, and
+// three vectors that every row fetches from L2, not memory (issue slots 65 % used,
+// DRAM 46 %).
 template <bool kLayer, typename T, typename H, int NV, bool kShift>
 __global__ void __launch_bounds__(1024) norm_tokens_kernel(const __grid_constant__ NormParams p) {
   __shared__ __align__(8) uint32_t buf[kExchange];
@@ -541,7 +543,7 @@ __global__ void __launch_bounds__(1024) norm_tokens_kernel(const __grid_constant
 // Many tokens of wide rows: persistent blocks whose rows arrive in a ring of
 // shared-memory stages by bulk copies, the next rows' while this one is worked
 // on, so memory does not wait for a statistic.  What bounds the norm is its four
-// reductions a row, since one block fills an SM (1001 x 11008 layer norms: 43
+// reductions a row, since one block fills an SM (1001 x 11008 layer norms: 44
 // us, the bytes alone 24).
 struct Ring {
   uint8_t* at;
@@ -803,7 +805,12 @@ int row_chunks(int d, int64_t tokens, int sms) {
 // ring more than once, and of those the rows so wide that few of their blocks
 // fit an SM.  Narrower rows overlap better as many blocks of one row each (norms
 // of 8000 x 4096 bf16 and quantized: streaming 60.9 us, else 51.6; 2000 x 8192
-// 41.3 and 32.6; but with both norms and a gate 2000 x 11008 45 and 61).  The
+// 41.3 and 32.6), but for some on an fp32 residual (both norms and a gate for
+// each token, 2000 x 4096 20.7 and 24.7).  Of wider rows, in registers at 32
+// elements a thread, those with a gate for each token lose (both norms, 2000 x
+// 11008 45 and 54 to 61 us, 8000 x 11008 155 and 187), those that are quantized
+// and layer norms without such a gate win (8000 x 11008: RMS and quantized 163
+// and 132, two layer norms 205 and 173), which this rule leaves there.  The
 // quantizer does so little for a row that of 16-bit types it streams from some
 // size on (8000 x 4096: 23.6 us, else 27.7; 2000 x 4096: 7.6 and 7.4; fp32
 // 8000 x 4096 29.8 and 28.3).

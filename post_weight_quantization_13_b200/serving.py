@@ -12,9 +12,13 @@ tensors the caller owns.
     h, xq = norm_tokens(h, y, weight, quantize=True)
     h, y = mlp_int8(h, y, weight, gate, up, down)  # a decoder block's MLP half
 
-Activations are 2-D, tokens in rows, rows contiguous (any row stride).  These
-are inference calls: a solved layer is frozen, and no gradient flows through
-them.
+Only layers with one scale for each output channel run here: one solved in
+groups of columns (``group_size`` 64 or 128, as a 4-bit checkpoint has it) is
+refused by ``int8_layer``.  Activations are 2-D, tokens in rows, rows contiguous
+(any row stride).  These are inference calls: a solved layer is frozen, and no
+gradient flows through them, whatever ``requires_grad`` says.  They do not wait
+for the device: a wait inside a kernel that gave up, and left a result
+incomplete, shows in ``gptq_int8_status`` only.
 """
 from __future__ import annotations
 
