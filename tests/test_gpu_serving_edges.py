@@ -269,3 +269,46 @@ def test_int8_layer_of_a_layer_solved_in_another_order(lib, bits):
     lib.gptq_dequantize_layer(r["qweight"], r["scales"], r["zeros"], r["g_idx"], bits, deq)
     z = torch.zeros(70, dtype=torch.int32, device="cuda") if layer.zero is None else layer.zero
     assert torch.equal(layer.scale[:, None] * (layer.weight.int() - z[:, None]).float(), deq)
+
+
+# --------------------------------------------------------------- the most tokens
+def test_the_largest_number_of_tokens(lib):
+    """2^26 tokens: their rows equal those of small calls."""
+    T, d, out = 1 << 26, 32, 3
+    gen = torch.Generator("cuda").manual_seed(41)
+    x = torch.empty(T, d, dtype=BF16, device="cuda").normal_(generator=gen)
+    layer = R.on_device(lib, R.random_layer(np.random.default_rng(43), out, d, True))
+    w = torch.rand(d, generator=gen, device="cuda").to(BF16)
+    y, z = lib.linear_int8(x, layer), lib.gated_int8(x, layer, layer)
+    h, t = lib.norm_tokens(x, x, w, quantize=True)
+    for first in (0, T // 2 - 77, T - 300):
+        rows = slice(first, first + 300)
+        assert torch.equal(y[rows], lib.linear_int8(x[rows], layer))
+        assert torch.equal(z[rows], lib.gated_int8(x[rows], layer, layer))
+        h1, t1 = lib.norm_tokens(x[rows], x[rows], w, quantize=True)
+        assert torch.equal(h[rows], h1) and all(torch.equal(a[rows], b) for a, b in zip(t, t1))
+    lib.gptq_int8_status()
+
+
+# --------------------------------------------------- broadcast gates, shared rows
+@pytest.mark.parametrize("tokens,d", [(5, 264), (700, 9000), (3000, 4001)])
+def test_a_gate_expanded_over_the_tokens_is_a_gate_for_channels(lib, tokens, d):
+    gen = torch.Generator("cuda").manual_seed(47)
+    h, y = (torch.randn(tokens, d, generator=gen, device="cuda").to(F16) for _ in range(2))
+    w, g = (torch.rand(d, generator=gen, device="cuda").to(F16) for _ in range(2))
+    want = lib.norm_tokens(h, y, w, gate=g)
+    for gate in (g.expand(tokens, d), g.repeat(tokens, 1)):
+        assert all(torch.equal(a, b) for a, b in zip(lib.norm_tokens(h, y, w, gate=gate), want))
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 3, 40, 700])
+def test_slices_of_tokens_and_of_layers_are_tokens_and_layers(lib, tokens):
+    rng = np.random.default_rng([53, tokens])
+    layer = R.on_device(lib, R.random_layer(rng, 300, 520, True))
+    t = lib.quantize_tokens(torch.from_numpy(rng.standard_normal((tokens + 9, 520)).astype(np.float32)).cuda())
+    y = lib.linear_int8(t, layer, dtype=F32)
+    part = lib.Int8Tokens(*(a[5:5 + tokens] for a in t))
+    rows = lib.Int8Layer(*(a[7:290] for a in layer))
+    assert torch.equal(lib.linear_int8(part, rows, dtype=F32), y[5:5 + tokens, 7:290])
+    assert torch.equal(lib.gated_int8(part, rows, rows, dtype=F32),
+                       lib.gated_int8(t, layer, layer, dtype=F32)[5:5 + tokens, 7:290])
